@@ -21,9 +21,11 @@
  *
  * Layout conventions (all entry points):
  *   - every q/k/v/out tensor is a contiguous bf16 array [batch, heads, L, d]
- *     (row-major, d fastest), L = T * H * W tokens, d in {64, 128}; the one
- *     exception is the raster side of the token-major reorders,
- *     [batch, L, heads, d];
+ *     (row-major, d fastest), L = T * H * W tokens, d in {64, 128}; the
+ *     exceptions are the raster side of the token-major reorders and the
+ *     tensors of differential attention with token_major set,
+ *     [batch, L, heads, d], and the plain [rows, cols] arrays of layer norm and
+ *     dropout, which may be bf16, fp16 or fp32;
  *   - raster order: token n = (t * H + h) * W + w;
  *   - tiled order: tiles in raster order over the tile grid, tokens in raster
  *     order inside a tile; tile i occupies rows [i * Ntile, (i + 1) * Ntile).
@@ -62,7 +64,8 @@ typedef enum {
   STA_ERR_CUDA = 8,      /* a CUDA runtime/driver call failed (message via sta_last_cuda_error) */
   STA_ERR_TIMEOUT = 9,   /* a kernel's bounded wait expired; the kernel gave up */
   STA_ERR_ARG = 10,      /* another argument is out of range (batch, heads, scale not finite ...) */
-  STA_ERR_SCRATCH = 11,  /* the work schedule does not fit the fixed scratch of sta_attention_fwd_noalloc */
+  STA_ERR_SCRATCH = 11,  /* the work schedule does not fit the fixed scratch of sta_attention_fwd_noalloc, or a
+                            workspace is smaller than its _workspace function says */
   STA_ERR_BOUNDS = 12    /* a device-side bounds check failed (libsta_checked.so only); the kernel skipped the access */
 } sta_status;
 
@@ -310,6 +313,133 @@ sta_status sta_attention_fwd_noalloc(const void* q, const void* k, const void* v
                                      int32_t batch, int32_t heads, int32_t d, sta_dim3 grid,
                                      sta_dim3 tile, const sta_dim3* window_per_head, float scale,
                                      void* stream);
+
+/*
+ * Differential attention over tile windows: the difference of two softmax maps,
+ * the second weighted by a learned number per head.  Each head's d columns of q
+ * and k hold two maps, columns 0 .. d/2 - 1 and d/2 .. d - 1; v keeps all d:
+ *   P_m  = softmax(scale * Q_m K_m^T) over the head's window of each query tile,
+ *   out  = (P_1 - lambda[head] P_2) V.
+ * Windows are those of sta_attention_fwd_raster: a grid that is not a tile
+ * multiple is padded with masking.  Nothing is cached per configuration: the
+ * kernel derives the windows itself, so calls of different shapes, streams and
+ * captured graphs share no state but the status word.
+ *   q, k, v, out: device bf16 in raster order, [batch, heads, L, d], or
+ *     [batch, L, heads, d] with token_major = 1; 16-byte aligned;
+ *   lambda: device fp32 [heads], any finite value;
+ *   out2: device bf16 shaped like out, receives P_2 V, or NULL;
+ *   lse: device fp32 [2, batch, heads, L] (raster order), receives the log-sum-exp
+ *     of scale * Q_m K_m^T over each row's window (natural log), or NULL.  The
+ *     backward needs out2 and lse;
+ *   d: 64 or 128 (32 or 64 columns per map); scale: finite and positive;
+ *   tile: th * tw divides 128 and tt is a multiple of 128 / (th * tw);
+ *   window_per_head: host array of `heads` entries, heads <= 256;
+ *   workspace: device memory of at least
+ *     sta_diff_attention_fwd_workspace(...) bytes (0 for short windows: may then
+ *     be NULL), 16-byte aligned, used until the call's kernels have run.  Calls
+ *     that may overlap on the GPU, and graphs that may run at the same time,
+ *     need a workspace each.
+ * The first library call on a device allocates the status word; make it before
+ * any stream capture.  batch = 0 or heads = 0 is a no-op.
+ * Errors: NULL, ALIGN, ALIAS (an output overlaps another buffer), SHAPE, WINDOW,
+ * HEADDIM, ARG, SCRATCH, ARCH, CUDA.
+ */
+sta_status sta_diff_attention_fwd(const void* q, const void* k, const void* v, const float* lambda, void* out,
+                                  void* out2, float* lse, int32_t batch, int32_t heads, int32_t d,
+                                  int32_t token_major, sta_dim3 grid, sta_dim3 tile,
+                                  const sta_dim3* window_per_head, float scale, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace sta_diff_attention_fwd needs (host only), or -1 on an invalid argument. */
+int64_t sta_diff_attention_fwd_workspace(int32_t batch, int32_t heads, int32_t d, sta_dim3 grid, sta_dim3 tile,
+                                         const sta_dim3* window_per_head);
+
+/*
+ * Backward of sta_diff_attention_fwd, with out, out2 and lse as it wrote them and
+ * dout the output gradient (laid out like out):
+ *   dP = dO V^T,  D_m = dO . (P_m V) per row,
+ *   dV = (P_1 - lambda P_2)^T dO,
+ *   dQ_1 = scale P_1 (dP - D_1) K_1,  dQ_2 = -lambda scale P_2 (dP - D_2) K_2,
+ *   dK_m the same with the transposes and Q_m,
+ *   dlambda[h] = - sum over batch and rows of D_2 (fp32, the sum taken from P_2 and
+ *   dP in fp32).
+ * P is rebuilt from lse; the products take P and dS rounded to bf16 and accumulate
+ * in fp32.  dq, dk, dv: device bf16 laid out like q; dlambda: device fp32 [heads].
+ * Every output element is written.  Deterministic: no atomics.
+ * workspace as above, sta_diff_attention_bwd_workspace(...) bytes.
+ */
+sta_status sta_diff_attention_bwd(const void* q, const void* k, const void* v, const float* lambda, const void* out,
+                                  const void* out2, const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                                  float* dlambda, int32_t batch, int32_t heads, int32_t d, int32_t token_major,
+                                  sta_dim3 grid, sta_dim3 tile, const sta_dim3* window_per_head, float scale,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
+
+int64_t sta_diff_attention_bwd_workspace(int32_t batch, int32_t heads, int32_t d, sta_dim3 grid, sta_dim3 tile,
+                                         const sta_dim3* window_per_head);
+
+/* Element types of layer norm and dropout. */
+typedef enum { STA_BF16 = 0, STA_FP16 = 1, STA_FP32 = 2 } sta_dtype;
+
+/*
+ * Layer norm over the columns of a contiguous [rows, cols] array, with an optional
+ * dropout and residual sum in front (the residual stream of a transformer block):
+ *   h = residual + dropout(x)   (h = x without them),
+ *   y = (h - mean) * rstd * weight + bias,
+ *   mean = sum h / cols,  rstd = 1 / sqrt(sum (h - mean)^2 / cols + eps),
+ * in fp32, y from h before h is rounded for its store.
+ *   x, residual (or NULL), y, h (or NULL): device arrays of `dtype`;
+ *   weight, bias (each may be NULL: 1 and 0): device [cols], of `param_dtype`, which
+ *     is `dtype` or STA_FP32;
+ *   mean, rstd: device fp32 [rows], or NULL;
+ *   dropout_p: probability of a zero, 0 .. 1 (0: no dropout, rng may be NULL), as in
+ *     sta_dropout, whose mask it is;
+ *   rng: device int64[2], seed and offset, read by the kernel (a captured graph
+ *     takes the values it finds there at each replay).
+ * Every pointer to an array with `cols` columns is 16-byte aligned, whatever cols
+ * is.  1 <= cols <= 16384.  rows = 0 is a no-op.  Outputs must not overlap inputs or
+ * one another.
+ * Errors: NULL, ALIGN, ALIAS, SHAPE, ARG, ARCH, CUDA.
+ */
+sta_status sta_layer_norm_fwd(const void* x, const void* residual, const void* weight, const void* bias, void* y,
+                              void* h, float* mean, float* rstd, int64_t rows, int32_t cols, int32_t dtype,
+                              int32_t param_dtype, float eps, float dropout_p, const int64_t* rng, void* stream);
+
+/*
+ * Backward of sta_layer_norm_fwd.  With z = (h - mean) * rstd and g = dy * weight:
+ *   dresidual = rstd * (g - sum g / cols - z * sum(g z) / cols) + dh,
+ *   dx = dresidual through the dropout mask (dx = dresidual without dropout),
+ *   dweight = sum over rows of dy * z,  dbias = sum over rows of dy.
+ *   dy, h: device arrays of `dtype`; mean, rstd: device fp32 [rows];
+ *   weight: as in the forward, or NULL for 1;
+ *   dh: the gradient that reaches h by the residual stream, or NULL for 0;
+ *   dx, dresidual: device arrays of `dtype`, either may be NULL, not both;
+ *   dweight, dbias: device [cols] of `param_dtype`, or NULL; summed in fp32, in a
+ *     fixed order;
+ *   workspace: sta_layer_norm_bwd_workspace(rows, cols) bytes, 16-byte aligned, used
+ *     until the call's kernels have run (needed only for dweight or dbias).
+ * rows = 0 sets dweight and dbias to zero.
+ */
+sta_status sta_layer_norm_bwd(const void* dy, const void* h, const float* mean, const float* rstd, const void* weight,
+                              const void* dh, void* dx, void* dresidual, void* dweight, void* dbias, int64_t rows,
+                              int32_t cols, int32_t dtype, int32_t param_dtype, float dropout_p, const int64_t* rng,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+int64_t sta_layer_norm_bwd_workspace(int64_t rows, int32_t cols);
+
+/*
+ * Dropout with a counter-based generator: y[r, c] = x[r, c] * s where kept, else 0.
+ * The mask is a function of (seed, offset, r, c) alone and is never stored; the
+ * backward is the same call on the gradient.  Element (r, c) takes 16-bit word
+ * c mod 8 of the Philox 4x32-10 block with counter (r * ceil(cols / 8) + c div 8,
+ * offset) and key seed; it is kept where that word >= round(65536 p), and
+ * s = 65536 / (65536 - round(65536 p)).  Dropped values are replaced, so an infinity
+ * or NaN there leaves a zero.
+ *   x, y: device arrays of `dtype`, contiguous [rows, cols], 16-byte aligned, not
+ *   overlapping; 0 <= dropout_p <= 1; rng: device int64[2], seed and offset.
+ * Errors: NULL, ALIGN, ALIAS, SHAPE, ARG, ARCH, CUDA.
+ */
+sta_status sta_dropout(const void* x, void* y, int64_t rows, int32_t cols, int32_t dtype, float dropout_p,
+                       const int64_t* rng, void* stream);
 
 /*
  * Synchronises `stream` and reports whether any kernel of this library on the

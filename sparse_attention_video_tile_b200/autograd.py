@@ -17,6 +17,10 @@ part of the reorders.  The tiled q, k, v, output and log-sum-exp are kept for
 the backward.  Tiles must hold a multiple of 128 tokens and the grid must be a
 tile multiple (the backward kernel's blocking).  The backward is not itself
 differentiable: a second derivative raises.
+
+``sta_diff_attention`` (differential attention over the same windows, any grid),
+``sta_layer_norm`` and ``sta_dropout`` are the other operators of such a block, each
+with its backward in the library's kernels.
 """
 from __future__ import annotations
 
@@ -25,8 +29,9 @@ from typing import Optional, Sequence
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (sta_attention_bwd, sta_attention_fwd_lse, sta_tile_reorder, sta_tile_reorder_tokens,
-               sta_tile_unorder, sta_tile_unorder_tokens)
+from . import (sta_attention_bwd, sta_attention_fwd_lse, sta_diff_attention_bwd, sta_diff_forward, sta_dropout_forward,
+               sta_layer_norm_bwd, sta_layer_norm_forward, sta_tile_reorder, sta_tile_reorder_tokens, sta_tile_unorder,
+               sta_tile_unorder_tokens)
 
 
 def _to_tiled(x, grid, tile, token_major: bool):
@@ -83,3 +88,110 @@ def sta_attention(q, k, v, grid, tile, window_per_head: Sequence, scale: Optiona
         scale = 1.0 / float(q.shape[-1]) ** 0.5
     return STAttentionFunction.apply(q, k, v, tuple(grid), tuple(tile),
                                      [tuple(w) for w in window_per_head], float(scale), bool(token_major))
+
+
+class STADiffAttentionFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, lam, grid, tile, windows, scale, token_major):
+        q, k, v, lam = (x.contiguous() for x in (q, k, v, lam))
+        out, out2, lse = sta_diff_forward(q, k, v, lam, grid, tile, windows, scale, token_major, save=True)
+        ctx.save_for_backward(q, k, v, lam, out, out2, lse)
+        ctx.sta_args = (grid, tile, windows, scale, token_major)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        q, k, v, lam, out, out2, lse = ctx.saved_tensors
+        grid, tile, windows, scale, token_major = ctx.sta_args
+        dq, dk, dv, dlam = (torch.empty_like(x) for x in (q, k, v, lam))
+        sta_diff_attention_bwd(q, k, v, lam, out, out2, lse, dout.to(torch.bfloat16).contiguous(), dq, dk, dv, dlam, grid,
+                               tile, windows, scale, token_major)
+        return dq, dk, dv, dlam, None, None, None, None, None
+
+
+class STALayerNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, residual, dropout_p, rng):
+        x = x.contiguous()
+        residual = None if residual is None else residual.contiguous()
+        rng = rng.clone() if dropout_p > 0 else None   # the backward's mask, whatever becomes of the caller's state
+        y, h, mean, rstd = sta_layer_norm_forward(x, weight, bias, eps, residual, dropout_p, rng)
+        ctx.save_for_backward(x if h is None else h, mean, rstd, weight, rng)
+        ctx.sta_args = (bias is not None, residual is not None, dropout_p, h is not None, None if bias is None else bias.dtype)
+        return (y, h) if h is not None else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, mean, rstd, weight, rng = ctx.saved_tensors
+        has_bias, has_res, p, _, bias_dtype = ctx.sta_args
+        dy = dy.to(h.dtype).contiguous()
+        dh = None if dh is None else dh.to(h.dtype).contiguous()
+        want_w = weight is not None and ctx.needs_input_grad[1]
+        want_b = has_bias and ctx.needs_input_grad[2]
+        dx = torch.empty_like(h)
+        dres = torch.empty_like(h) if has_res and p > 0 else None
+        pd = weight.dtype if weight is not None else bias_dtype
+        dw = torch.empty(h.shape[-1], dtype=pd, device=h.device) if want_w else None
+        db = torch.empty(h.shape[-1], dtype=pd, device=h.device) if want_b else None
+        sta_layer_norm_bwd(dy, h, mean, rstd, weight, dx, dres, dw, db, dh, p, rng)
+        return dx, dw, db, None, ((dx if dres is None else dres) if has_res else None), None, None
+
+
+class STADropoutFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, dropout_p, rng):
+        rng = rng.clone()
+        ctx.save_for_backward(rng)
+        ctx.dropout_p = dropout_p
+        return sta_dropout_forward(x.contiguous(), dropout_p, rng)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        (rng,) = ctx.saved_tensors
+        return sta_dropout_forward(dy.contiguous(), ctx.dropout_p, rng), None, None
+
+
+def sta_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, dropout_p: float = 0.0, rng=None):
+    """Layer norm over the last dimension of h = residual + dropout(x), with gradients:
+    CUDA tensors in bf16, fp16 or fp32, weight and bias in the same type or fp32.
+    Returns y, or (y, h) when there is a residual or dropout (h is the residual stream;
+    its gradient flows back through the same kernel).  ``rng``: int64 CUDA tensor
+    [seed, offset]; give each call of a step its own offset."""
+    if dropout_p > 0 and rng is None:
+        raise ValueError("dropout needs rng, an int64 CUDA tensor [seed, offset]")
+    return STALayerNormFunction.apply(x, weight, bias, float(eps), residual, float(dropout_p), rng)
+
+
+def sta_dropout(x, dropout_p: float, rng):
+    """Dropout with gradients; the mask is a function of ``rng`` (int64 CUDA tensor
+    [seed, offset]) and the element's place (rows over the last dimension), and is
+    evaluated again in the backward."""
+    if dropout_p == 0:
+        return x
+    return STADropoutFunction.apply(x, float(dropout_p), rng)
+
+
+def sta_diff_attention(q, k, v, lam, grid, tile, window_per_head: Sequence, scale: Optional[float] = None,
+                       token_major: bool = False, norm_weight=None, norm_bias=None, eps: float = 1e-5,
+                       dropout_p: float = 0.0, rng=None):
+    """Differential attention over tile windows with a backward: bf16 CUDA tensors in
+    raster order, [B, heads, L, d] or, with ``token_major``, [B, L, heads, d]; output in
+    the same layout.  out = (softmax(scale Q1 K1^T) - lam softmax(scale Q2 K2^T)) V with
+    Q1, K1 the first d/2 columns of q and k, Q2, K2 the last d/2, ``lam`` fp32 [heads]
+    (any function of learned vectors; it receives a gradient) and scale 1 / sqrt(d / 2)
+    by default.  Grids that are not tile multiples are padded with masking.
+
+    With ``norm_weight`` (and ``norm_bias``), both [d], every head's output row then
+    goes through ``sta_layer_norm``, as the method normalises its heads (a factor such as
+    1 - lambda_init belongs in the weight), and with ``dropout_p`` > 0 through
+    ``sta_dropout`` with ``rng``."""
+    if scale is None:
+        scale = 1.0 / float(q.shape[-1] // 2) ** 0.5
+    out = STADiffAttentionFunction.apply(q, k, v, lam, tuple(grid), tuple(tile), [tuple(w) for w in window_per_head],
+                                         float(scale), bool(token_major))
+    if norm_weight is not None or norm_bias is not None:
+        out = sta_layer_norm(out, norm_weight, norm_bias, eps)
+    return sta_dropout(out, dropout_p, rng) if dropout_p > 0 else out

@@ -16,20 +16,7 @@
 #include "internal.h"
 
 namespace sta {
-namespace {
 
-thread_local std::string g_last_cuda_error;
-
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per bounded wait
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void* a, const void* b, int64_t bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + static_cast<uintptr_t>(bytes) && y < x + static_cast<uintptr_t>(bytes);
-}
-
-// Device check: compute capability 10.0 (B200, sm_100a code).
 sta_status check_device(int* dev_out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -40,6 +27,17 @@ sta_status check_device(int* dev_out) {
   if (major != 10 || minor != 0) return STA_ERR_ARCH;
   if (dev_out) *dev_out = dev;
   return STA_OK;
+}
+
+namespace {
+
+thread_local std::string g_last_cuda_error;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool overlaps(const void* a, const void* b, int64_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(bytes) && y < x + static_cast<uintptr_t>(bytes);
 }
 
 // ---------------------------------------------------------------- per-device state
@@ -188,6 +186,14 @@ sta_status validate_tensor_args(const void* src, const void* dst, int64_t batch_
 sta_status cuda_fail(cudaError_t e) {
   g_last_cuda_error = cudaGetErrorString(e);
   return STA_ERR_CUDA;
+}
+
+sta_status status_word(int dev, int32_t** word) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* st = nullptr;
+  const sta_status s = device_state(dev, &st);
+  if (s == STA_OK) *word = st->d_err;
+  return s;
 }
 
 }  // namespace sta

@@ -143,6 +143,16 @@ cudaError_t launch_backward(const void* q, const void* k, const void* v, const v
 
 cudaError_t launch_selftest_wait(int32_t* err_flag, uint64_t limit_ns, cudaStream_t stream);
 
+// STA_OK on compute capability 10.0 (B200, sm_100a code), with the current device's
+// number; else STA_ERR_ARCH or STA_ERR_CUDA (api.cu).
+sta_status check_device(int* dev_out);
+
+// Device `dev`'s bounded-wait status word, allocated on the first call (api.cu).
+sta_status status_word(int dev, int32_t** word);
+
+// Time a bounded wait of the library's kernels may take.
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+
 // Records the text of a failed CUDA call for sta_last_cuda_error and returns
 // STA_ERR_CUDA (api.cu).
 sta_status cuda_fail(cudaError_t e);
