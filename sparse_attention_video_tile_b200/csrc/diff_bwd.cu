@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (lane == 0 && warp == 10) {
       // ---------------------------------------------------------- S_1, S_2, dP
       constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
-      const uint64_t dq = sdesc_sw128(sb + S::kQ, 16, 1024), ddo = sdesc_sw128(sb + S::kDo, 16, 1024);
-      const uint64_t dk0 = sdesc_sw128(sb + S::kK, 16, 1024), dv0 = sdesc_sw128(sb + S::kV, 16, 1024);
+      const uint32_t dq = desc_lo(sb + S::kQ, kLboK), ddo = desc_lo(sb + S::kDo, kLboK);
+      const uint32_t dk0 = desc_lo(sb + S::kK, kLboK), dv0 = desc_lo(sb + S::kV, kLboK);
       uint32_t seq = 0, k = 0;
       bool ok = true;
       for (int32_t idx = first; ok && idx < p.n_items; idx += stride, ++k) {
@@ -282,25 +282,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int32_t j = 0; ok && j < it.n; ++j, ++seq) {
           const uint32_t st = seq % KS, ph = (seq / KS) & 1;
           ok = mbar_wait(sb + S::kKFull + 8 * st, ph, wc, 0x35);
-          const uint64_t dk = dk0 + st * (S::kBlk >> 4), dv = dv0 + st * (S::kBlk >> 4);
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
+          const uint32_t dk = dk0 + st * (S::kBlk >> 4), dv = dv0 + st * (S::kBlk >> 4);
+          static_for<2>([&](auto M) {
+            constexpr int m = decltype(M)::value;
             // the buffer's scores (map 2 of the last block, then map 1 of this one) are in registers
             if (ok && (m == 1 || seq > 0))
               ok = mbar_wait(sb + S::kSFree + 8 * (1 - m), (m == 1 ? seq : seq - 1) & 1, wc, 0x36);
-            if (!ok) break;
+            if (!ok) return;
             tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              umma_ss(tmem, dq + koff(m * (D / 32) + i), dk + koff(m * (D / 32) + i), idesc, i > 0);
+            static_for<D / 32>([&](auto I) {
+              constexpr uint32_t o = koff(m * (D / 32) + decltype(I)::value);
+              mma_ss<o, o>(tmem, dq, dk, idesc, decltype(I)::value > 0);
+            });
             umma_commit(sb + S::kSFull + 8 * m);
-          }
+          });
           ok = ok && mbar_wait(sb + S::kVFull + 8 * st, ph, wc, 0x37) &&
                (seq == 0 || mbar_wait(sb + S::kPFree, (seq - 1) & 1, wc, 0x38));
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) umma_ss(tmem + 128, ddo + koff(i), dv + koff(i), idesc, i > 0);
+          static_for<D / 16>([&](auto I) {
+            constexpr uint32_t o = koff(decltype(I)::value);
+            mma_ss<o, o>(tmem + 128, ddo, dv, idesc, decltype(I)::value > 0);
+          });
           umma_commit(sb + S::kVEmpty + 8 * st);
           if (j + 1 == it.n) umma_commit(sb + S::kFixEmpty);
           umma_commit(sb + S::kPFull);
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // B is the 64-column box that holds K_m; at d = 64 both maps share the only box and
       // the other map's half of the product is left unread.
       constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false, true);
-      const uint64_t dk0 = sdesc_sw128(sb + S::kK, kBlockRows * 128, 1024);
+      const uint32_t dk0 = desc_lo(sb + S::kK, kLboMn);
       uint32_t seq = 0;
       bool ok = true;
       for (int32_t idx = first; ok && idx < p.n_items; idx += stride) {
@@ -327,11 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && mbar_wait(sb + S::kDsFull + 8 * m, seq & 1, wc, 0x39);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t dk = dk0 + st * (S::kBlk >> 4) + (D == 128 ? m * (16384 >> 4) : 0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              umma_ts(tmem + 384 + 64 * m, tmem + 256 + 64 * m + 8 * i, dk + static_cast<uint64_t>(i * (2048 >> 4)), idesc,
-                      (j > 0 || i > 0));
+            const uint32_t dk = dk0 + st * (S::kBlk >> 4) + (D == 128 ? m * (16384 >> 4) : 0);
+            static_for<8>([&](auto I) {
+              constexpr int i = decltype(I)::value;
+              mma_ts<8 * i, mnoff(i)>(tmem + 384 + 64 * m, tmem + 256 + 64 * m, dk, idesc, (j > 0 || i > 0));
+            });
             umma_commit(sb + S::kDsDone + 8 * m);
           }
           if (!ok) break;
@@ -461,16 +464,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 struct Dkv {
   static constexpr int kBlk = kBlockRows * D * 2;
-  static constexpr int kStages = D == 64 ? 4 : 2;
-  static constexpr int kStage = 2 * kBlk;                  // Q and dO
-  static constexpr int kK = 0, kV = kBlk, kRing = 2 * kBlk;
-  static constexpr int kDs = kRing + kStages * kStage;     // dS_2^T: two boxes of 128 rows x 64 columns
+  static constexpr int kQs = D == 64 ? 4 : 3;              // stages of Q
+  static constexpr int kOs = D == 64 ? 4 : 1;              // stages of dO
+  static constexpr int kK = 0, kV = kBlk, kQ = 2 * kBlk, kDo = kQ + kQs * kBlk;
+  static constexpr int kDs = kDo + kOs * kBlk;             // dS_2^T: two boxes of 128 rows x 64 columns
   static constexpr int kLse = kDs + 32768;                 // float [map][query]
   static constexpr int kD = kLse + 1024;                   // float [map][query]
   static constexpr int kBar = kD + 1024;
   static constexpr int kFixFull = kBar, kFixEmpty = kFixFull + 8;
-  static constexpr int kFull = kFixEmpty + 8, kEmpty = kFull + 8 * kStages;
-  static constexpr int kLFull = kEmpty + 8 * kStages, kLEmpty = kLFull + 8;
+  static constexpr int kQFull = kFixEmpty + 8, kQEmpty = kQFull + 8 * kQs;
+  static constexpr int kDoFull = kQEmpty + 8 * kQs, kDoEmpty = kDoFull + 8 * kOs;
+  static constexpr int kLFull = kDoEmpty + 8 * kOs, kLEmpty = kLFull + 8;
   static constexpr int kDFull = kLEmpty + 8, kDEmpty = kDFull + 8;
   static constexpr int kSFull = kDEmpty + 8, kSFree = kSFull + 16;    // [map]
   static constexpr int kPFull = kSFree + 16;               // dP^T written
@@ -487,7 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ BwdParams p) {
   using S = Dkv<D>;
-  constexpr int KS = S::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   if ((sb & 1023u) != 0) {   // no room for a pad: report instead of computing with a wrong swizzle
@@ -499,9 +502,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(sb + S::kFixFull, 1);
     mbar_init(sb + S::kFixEmpty, 1);
-    for (int i = 0; i < KS; ++i) {
-      mbar_init(sb + S::kFull + 8 * i, 1);
-      mbar_init(sb + S::kEmpty + 8 * i, 1);
+    for (int i = 0; i < S::kQs; ++i) {
+      mbar_init(sb + S::kQFull + 8 * i, 1);
+      mbar_init(sb + S::kQEmpty + 8 * i, 1);
+    }
+    for (int i = 0; i < S::kOs; ++i) {
+      mbar_init(sb + S::kDoFull + 8 * i, 1);
+      mbar_init(sb + S::kDoEmpty + 8 * i, 1);
     }
     mbar_init(sb + S::kLFull, 1);
     mbar_init(sb + S::kLEmpty, 8);
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     setmaxnreg_dec<kRegsOther>();
     if (lane == 0 && warp == 8) {
-      // ---------------------------------------------------------- K, V of the item; Q, dO of its blocks
+      // ---------------------------------------------------------- K, V of the item; Q of its blocks
       uint32_t seq = 0, k = 0;
       bool ok = true;
       for (int32_t idx = first; ok && idx < p.n_items; idx += stride) {
@@ -547,18 +554,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_block<D>(g, sb + S::kV, &tm_v, sb + S::kFixFull, it, own_block(it), true);
         Block b = first_block(it);
         for (int32_t j = 0; j < it.n; ++j, ++seq, next_block(g, it, b)) {
-          const uint32_t st = seq % KS, full = sb + S::kFull + 8 * st, base = sb + S::kRing + st * S::kStage;
-          ok = mbar_wait(sb + S::kEmpty + 8 * st, ((seq / KS) & 1) ^ 1, wc, 0x42);
+          const uint32_t st = seq % S::kQs;
+          ok = mbar_wait(sb + S::kQEmpty + 8 * st, ((seq / S::kQs) & 1) ^ 1, wc, 0x42);
           if (!ok) break;
-          mbar_arrive_expect_tx(full, 2 * S::kBlk);
-          load_block<D>(g, base, &tm_q, full, it, b, true);
-          load_block<D>(g, base + S::kBlk, &tm_do, full, it, b, true);
+          mbar_arrive_expect_tx(sb + S::kQFull + 8 * st, S::kBlk);
+          load_block<D>(g, sb + S::kQ + st * S::kBlk, &tm_q, sb + S::kQFull + 8 * st, it, b, true);
         }
       }
       if (k > 0) mbar_wait_drain(sb + S::kFixFull, (k - 1) & 1, p.limit_ns);
-      for (uint32_t i = 0; i < KS && i < seq; ++i) {
-        const uint32_t last = seq - 1 - ((seq - 1 - i) % KS);
-        mbar_wait_drain(sb + S::kFull + 8 * i, (last / KS) & 1, p.limit_ns);
+      for (uint32_t i = 0; i < S::kQs && i < seq; ++i) {
+        const uint32_t last = seq - 1 - ((seq - 1 - i) % S::kQs);
+        mbar_wait_drain(sb + S::kQFull + 8 * i, (last / S::kQs) & 1, p.limit_ns);
+      }
+    } else if (lane == 0 && warp == 10) {
+      // ---------------------------------------------------------- dO of the blocks
+      uint32_t seq = 0;
+      bool ok = true;
+      for (int32_t idx = first; ok && idx < p.n_items; idx += stride) {
+        const Item it = get_item<true>(g, idx);
+        Block b = first_block(it);
+        for (int32_t j = 0; j < it.n; ++j, ++seq, next_block(g, it, b)) {
+          const uint32_t st = seq % S::kOs;
+          ok = mbar_wait(sb + S::kDoEmpty + 8 * st, ((seq / S::kOs) & 1) ^ 1, wc, 0x4f);
+          if (!ok) break;
+          mbar_arrive_expect_tx(sb + S::kDoFull + 8 * st, S::kBlk);
+          load_block<D>(g, sb + S::kDo + st * S::kBlk, &tm_do, sb + S::kDoFull + 8 * st, it, b, true);
+        }
+      }
+      for (uint32_t i = 0; i < S::kOs && i < seq; ++i) {
+        const uint32_t last = seq - 1 - ((seq - 1 - i) % S::kOs);
+        mbar_wait_drain(sb + S::kDoFull + 8 * i, (last / S::kOs) & 1, p.limit_ns);
       }
     } else if (lane == 0 && warp == 11) {
       // ---------------------------------------------------------- -lse and -D of the blocks
@@ -588,29 +613,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seq > 0) mbar_wait_drain(sb + S::kDFull, (seq - 1) & 1, p.limit_ns);
     } else if (lane == 0 && warp == 9) {
       // ---------------------------------------------------------- MMAs, all from one thread
-      // Steady state per block i: S_1 of i + 1 | dV, dK_1 of i | S_2 of i + 1 | dK_2 of i | dP of
-      // i + 1.  MMAs of one thread execute in order, so dP may overwrite the columns that dV
+      // Steady state per block i: S_1 of i + 1 | dV of i | S_2 of i + 1 | dK_1 of i | dP of i + 1 |
+      // dK_2 of i.  MMAs of one thread execute in order, so dP may overwrite the columns that dV
       // and dK_1 read.  S_2 of i + 1 sits between the accumulations: the warps have loaded S_1
-      // by then and work on its exponentials.
+      // by then and work on its exponentials.  dK_2 reads shared memory and comes last: its
+      // operand is overwritten only at the end of the next block's elementwise step.
       constexpr uint32_t id_ss = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t id_dv = idesc_bf16_f32(128, D, false, true);
       constexpr uint32_t id_dk = idesc_bf16_f32(128, 64, false, true);
-      const uint64_t dk = sdesc_sw128(sb + S::kK, 16, 1024), dv = sdesc_sw128(sb + S::kV, 16, 1024);
-      const uint64_t dds = sdesc_sw128(sb + S::kDs, 16, 1024);
-      const uint64_t dring = sdesc_sw128(sb + S::kRing, 16, 1024);                     // K-major
-      const uint64_t dring_mn = sdesc_sw128(sb + S::kRing, kBlockRows * 128, 1024);    // MN-major
-      auto ring_full = [&](uint32_t i) { return mbar_wait(sb + S::kFull + 8 * (i % KS), (i / KS) & 1, wc, 0x45); };
-      auto stage = [&](uint32_t i) -> uint64_t { return (i % KS) * static_cast<uint64_t>(S::kStage >> 4); };
-      auto issue_s = [&](uint32_t i, int m) {
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x)
-          umma_ss(tmem, dk + koff(m * (D / 32) + x), dring + stage(i) + koff(m * (D / 32) + x), id_ss, x > 0);
+      const uint32_t dk = desc_lo(sb + S::kK, kLboK), dv = desc_lo(sb + S::kV, kLboK), dds = desc_lo(sb + S::kDs, kLboK);
+      const uint32_t dq = desc_lo(sb + S::kQ, kLboK), ddo = desc_lo(sb + S::kDo, kLboK);
+      constexpr uint32_t kMn = ((kLboMn - kLboK) >> 4) << 16;   // K-major to MN-major low word
+      auto q_full = [&](uint32_t i) { return mbar_wait(sb + S::kQFull + 8 * (i % S::kQs), (i / S::kQs) & 1, wc, 0x45); };
+      auto do_full = [&](uint32_t i) { return mbar_wait(sb + S::kDoFull + 8 * (i % S::kOs), (i / S::kOs) & 1, wc, 0x50); };
+      auto q_at = [&](uint32_t i) -> uint32_t { return dq + (i % S::kQs) * (S::kBlk >> 4); };
+      auto do_at = [&](uint32_t i) -> uint32_t { return ddo + (i % S::kOs) * (S::kBlk >> 4); };
+      auto issue_s = [&](uint32_t i, auto M) {
+        constexpr int m = decltype(M)::value;
+        const uint32_t q = q_at(i);
+        static_for<D / 32>([&](auto X) {
+          constexpr uint32_t o = koff(m * (D / 32) + decltype(X)::value);
+          mma_ss<o, o>(tmem, dk, q, id_ss, decltype(X)::value > 0);
+        });
         umma_commit(sb + S::kSFull + 8 * m);
       };
       auto issue_dp = [&](uint32_t i) {
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x)
-          umma_ss(tmem + 128, dv + koff(x), dring + stage(i) + (S::kBlk >> 4) + koff(x), id_ss, x > 0);
+        const uint32_t d = do_at(i);
+        static_for<D / 16>([&](auto X) {
+          constexpr uint32_t o = koff(decltype(X)::value);
+          mma_ss<o, o>(tmem + 128, dv, d, id_ss, decltype(X)::value > 0);
+        });
         umma_commit(sb + S::kPFull);
       };
       uint32_t i = 0;   // block of the CTA's stream
@@ -618,56 +650,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int32_t idx = first; ok && idx < p.n_items; idx += stride, ++k) {
         const Item it = get_item<true>(g, idx);
-        ok = mbar_wait(sb + S::kFixFull, k & 1, wc, 0x46) && ring_full(i) &&
+        ok = mbar_wait(sb + S::kFixFull, k & 1, wc, 0x46) && q_full(i) && do_full(i) &&
              (i == 0 || mbar_wait(sb + S::kSFree + 8, (i - 1) & 1, wc, 0x47));
         if (!ok) break;
         tc_fence_after();
-        issue_s(i, 0);
+        issue_s(i, Const<0>{});
         issue_dp(i);
         ok = mbar_wait(sb + S::kSFree, i & 1, wc, 0x48);
         if (!ok) break;
         tc_fence_after();
-        issue_s(i, 1);
+        issue_s(i, Const<1>{});
         if (it.n == 1) umma_commit(sb + S::kFixEmpty);
         for (int32_t j = 0; j < it.n; ++j, ++i) {
           const bool more = j + 1 < it.n;
           if (more) {
-            ok = ring_full(i + 1) && mbar_wait(sb + S::kSFree + 8, i & 1, wc, 0x47);
+            ok = q_full(i + 1) && mbar_wait(sb + S::kSFree + 8, i & 1, wc, 0x47);
             if (!ok) break;
             tc_fence_after();
-            issue_s(i + 1, 0);
+            issue_s(i + 1, Const<0>{});
           }
           ok = mbar_wait(sb + S::kDsFull, i & 1, wc, 0x49);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t dqm = dring_mn + stage(i), dom = dqm + (S::kBlk >> 4);
+          const uint32_t dqm = q_at(i) + kMn, dom = do_at(i) + kMn;
           // P^T and dS_1^T of 16 queries x: 8 columns each of the dP region
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            umma_ts(tmem + 256, tmem + 128 + (x >> 2) * 64 + ((x >> 1) & 1) * 32 + (x & 1) * 8,
-                    dom + static_cast<uint64_t>(x * (2048 >> 4)), id_dv, (j > 0 || x > 0));
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            umma_ts(tmem + 384, tmem + 128 + (x >> 2) * 64 + ((x >> 1) & 1) * 32 + 16 + (x & 1) * 8,
-                    dqm + static_cast<uint64_t>(x * (2048 >> 4)), id_dk, (j > 0 || x > 0));
+          static_for<8>([&](auto X) {
+            constexpr int x = decltype(X)::value;
+            mma_ts<(x >> 2) * 64 + ((x >> 1) & 1) * 32 + (x & 1) * 8, mnoff(x)>(tmem + 256, tmem + 128, dom, id_dv,
+                                                                               (j > 0 || x > 0));
+          });
+          umma_commit(sb + S::kDoEmpty + 8 * (i % S::kOs));   // dP of block i was issued before
           if (more) {
             ok = mbar_wait(sb + S::kSFree, (i + 1) & 1, wc, 0x48);
             if (!ok) break;
             tc_fence_after();
-            issue_s(i + 1, 1);
+            issue_s(i + 1, Const<1>{});
           }
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            umma_ss(tmem + 448, dds + koff(x), dqm + (D == 128 ? (16384 >> 4) : 0) + static_cast<uint64_t>(x * (2048 >> 4)),
-                    id_dk, (j > 0 || x > 0));
-          umma_commit(sb + S::kDsDone);
-          umma_commit(sb + S::kEmpty + 8 * (i % KS));
+          static_for<8>([&](auto X) {
+            constexpr int x = decltype(X)::value;
+            mma_ts<(x >> 2) * 64 + ((x >> 1) & 1) * 32 + 16 + (x & 1) * 8, mnoff(x)>(tmem + 384, tmem + 128, dqm, id_dk,
+                                                                                    (j > 0 || x > 0));
+          });
           if (more) {
+            ok = do_full(i + 1);
+            if (!ok) break;
+            tc_fence_after();
             issue_dp(i + 1);
             if (j + 2 == it.n) umma_commit(sb + S::kFixEmpty);
-          } else {
-            umma_commit(sb + S::kOFull);
           }
+          static_for<8>([&](auto X) {
+            constexpr int x = decltype(X)::value;
+            mma_ss<koff(x), (D == 128 ? (16384 >> 4) : 0) + mnoff(x)>(tmem + 448, dds, dqm, id_dk, (j > 0 || x > 0));
+          });
+          umma_commit(sb + S::kDsDone);
+          umma_commit(sb + S::kQEmpty + 8 * (i % S::kQs));
+          if (!more) umma_commit(sb + S::kOFull);
         }
       }
       umma_commit(sb + S::kDrain);
@@ -679,19 +716,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hh = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t tS = tl + 64 * hh, tP = tl + 128 + 64 * hh;
-    const Local loc = local_of(g, row);
-    uint8_t* ds_row = smem + S::kDs + hh * 16384 + row * 128;
-    const ulonglong2* lse2 = reinterpret_cast<const ulonglong2*>(smem + S::kLse) + 16 * hh;   // two pairs of queries each
-    const ulonglong2* dd2 = reinterpret_cast<const ulonglong2*>(smem + S::kD) + 16 * hh;
+    // Scores are read as 16 x 8 fragments (two lane halves L, eight tiles j): this thread has the
+    // queries 8 j + 2 (lane mod 4) and the next, of 4 key rows, so -lse and -D are read once for
+    // 4 rows.  (With a row per thread every thread read them for all 64 queries: 1200 of the
+    // block's clocks of shared memory bandwidth, which the MMAs' operands need.)
+    const uint32_t ds_at = sb + S::kDs + hh * 16384 + (quad * 32 + (lane >> 2)) * 128 + (lane & 3) * 4;
+    const uint32_t vec_lane = sb + S::kLse + 256 * hh + 8 * (lane & 3);   // this thread's queries of tile 0
     const uint64_t sl2x2 = f32x2(p.scale_log2, p.scale_log2);
+    constexpr uint32_t kHalf = 16u << 16;   // TMEM address of lane 16
     uint32_t seq = 0, k = 0;
     bool ok = true;
     for (int32_t idx = first; ok && idx < p.n_items; idx += stride, ++k) {
-      const Item it = get_item<true>(g, idx);
-      const float nlam = -__ldg(p.lam + it.head);
-      const uint64_t nlam2 = f32x2(nlam, nlam);
-      for (int32_t j = 0; j < it.n; ++j, ++seq) {
-        uint64_t pr[2][32];   // P_1 and -lambda P_2, pairs of queries
+      // the loop keeps two numbers of the item: the block's P of both maps needs the registers
+      int32_t n;
+      uint64_t nlam2;
+      {
+        const Item it = get_item<true>(g, idx);
+        const float nlam = -__ldg(p.lam + it.head);
+        n = it.n;
+        nlam2 = f32x2(nlam, nlam);
+      }
+      for (int32_t j = 0; j < n; ++j, ++seq) {
+        uint64_t pr[2][32];   // P_1 and -lambda P_2: [16 L + 2 tile + row half], pairs of queries
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           ok = __all_sync(0xffffffffu, mbar_wait(sb + S::kSFull + 8 * m, seq & 1, wc, 0x4a) &&
@@ -699,63 +745,75 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           uint32_t s[64];
-          tmem_ld32_at<0>(tS, s);
-          tmem_ld32_at<32>(tS + 32, s);
+          tmem_ld_frag8<0>(tS, s);
+          tmem_ld_frag8<32>(tS + kHalf, s);
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(sb + S::kSFree + 8 * m);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const ulonglong2 nl = lse2[32 * m + x];
+          for (int x = 0; x < 8; ++x) {
+            const uint64_t nl = lds64(vec_lane + 512 * m + 32 * x);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float a, b;
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[4 * x + 2 * y]), __uint_as_float(s[4 * x + 2 * y + 1])), sl2x2,
-                                    y == 0 ? nl.x : nl.y),
-                          a, b);
-              const uint64_t e = f32x2(ex2_approx(a), ex2_approx(b));
-              pr[m][2 * x + y] = m == 0 ? e : mul_f32x2(e, nlam2);
-            }
+            for (int L = 0; L < 2; ++L)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int r = 32 * L + 4 * x + 2 * y;
+                float a, b;
+                f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[r]), __uint_as_float(s[r + 1])), sl2x2, nl), a, b);
+                const uint64_t e = f32x2(ex2_approx(a), ex2_approx(b));
+                pr[m][r / 2] = m == 0 ? e : mul_f32x2(e, nlam2);
+              }
           }
         }
         if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(sb + S::kLEmpty);
-        ok = __all_sync(0xffffffffu, mbar_wait(sb + S::kPFull, seq & 1, wc, 0x4c) && mbar_wait(sb + S::kDFull, seq & 1, wc, 0x4d) &&
-                                         (seq == 0 || mbar_wait(sb + S::kDsDone, (seq - 1) & 1, wc, 0x4e)));
+        ok = __all_sync(0xffffffffu, mbar_wait(sb + S::kPFull, seq & 1, wc, 0x4c) && mbar_wait(sb + S::kDFull, seq & 1, wc, 0x4d));
         if (!ok) break;
         tc_fence_after();
+        uint32_t d2[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t dp[32], pk[16], d1[16], d2[16];
-          tmem_ld32(tP + 32 * c, dp);
-          tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const ulonglong2 n1 = dd2[8 * c + x], n2 = dd2[32 + 8 * c + x];
+          for (int L = 0; L < 2; ++L) {
+            uint32_t dp[16], pk[8], d1[8];
+            tmem_ld_frag4(tP + 32 * c + L * kHalf, dp);
+            tmem_wait_ld();
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int q = 2 * x + y;
-              const uint64_t g2 = f32x2(__uint_as_float(dp[2 * q]), __uint_as_float(dp[2 * q + 1]));
-              const uint64_t p1 = pr[0][16 * c + q], p2 = pr[1][16 * c + q];
-              float a, b;
-              f32x2_split(add_f32x2(p1, p2), a, b);
-              pk[q] = pack_bf16x2(a, b);
-              f32x2_split(mul_f32x2(p1, add_f32x2(g2, y == 0 ? n1.x : n1.y)), a, b);
-              d1[q] = pack_bf16x2(a, b);
-              f32x2_split(mul_f32x2(p2, add_f32x2(g2, y == 0 ? n2.x : n2.y)), a, b);
-              d2[q] = pack_bf16x2(a, b);
+            for (int x = 0; x < 4; ++x) {
+              const uint64_t n1 = lds64(vec_lane + 1024 + 32 * (4 * c + x)), n2 = lds64(vec_lane + 1536 + 32 * (4 * c + x));
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int q = 16 * L + 2 * (4 * c + x) + y;
+                const uint64_t g2 = f32x2(__uint_as_float(dp[4 * x + 2 * y]), __uint_as_float(dp[4 * x + 2 * y + 1]));
+                const uint64_t p1 = pr[0][q], p2 = pr[1][q];
+                float a, b;
+                f32x2_split(add_f32x2(p1, p2), a, b);
+                pk[2 * x + y] = pack_bf16x2(a, b);
+                f32x2_split(mul_f32x2(p1, add_f32x2(g2, n1)), a, b);
+                d1[2 * x + y] = pack_bf16x2(a, b);
+                f32x2_split(mul_f32x2(p2, add_f32x2(g2, n2)), a, b);
+                d2[q] = pack_bf16x2(a, b);
+              }
             }
+            tmem_st_frag4(tP + 32 * c + L * kHalf, pk);
+            tmem_st_frag4(tP + 32 * c + 16 + L * kHalf, d1);
           }
-          tmem_st16(tP + 32 * c, pk);
-          tmem_st16(tP + 32 * c + 16, d1);
-          // 16-byte chunk x (8 queries) of the row's 128 bytes, at its swizzled place
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<uint4*>(ds_row + (((4 * c + x) ^ (row & 7)) << 4)) =
-                make_uint4(d2[4 * x], d2[4 * x + 1], d2[4 * x + 2], d2[4 * x + 3]);
         }
+        // the last block's dK_2 has read dS_2^T; a tile's 8 queries are one 16-byte chunk of a row,
+        // at its swizzled place (rows 8 apart share the swizzle)
+        if (seq > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(sb + S::kDsDone, (seq - 1) & 1, wc, 0x4e));
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int L = 0; L < 2; ++L)
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              sts32(ds_at + (16 * L + 8 * y) * 128 + ((x ^ (lane >> 2)) << 4), d2[16 * L + 2 * x + y]);
         tmem_wait_st();
         fence_proxy_async();
         tc_fence_before();
@@ -769,7 +827,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(sb + S::kOFull, k & 1, wc, 0x4f));
       if (!ok) break;
       tc_fence_after();
-      const int32_t token = token_of(g, own_block(it), loc);
+      const Item it = get_item<true>(g, idx);
+      const int32_t token = token_of(g, own_block(it), local_of(g, row));
       const int64_t at = row_of(g, it.b, it.head, token >= 0 ? token : 0) * D + hh * (D / 2);
       store_half<D / 2>(tl + 384 + 64 * hh + (D == 64 ? 32 * hh : 0), p.o0 + at, p.scale, token >= 0);
       store_half<D / 2>(tl + 256 + hh * (D / 2), p.o1 + at, 1.0f, token >= 0);

@@ -32,6 +32,51 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// TMEM tiles of 16 lanes x 8 columns of 32 bits, spread over a warp like a matrix
+// fragment: thread t holds columns 2 (t mod 4) and the next of rows t / 4 (first two
+// registers of a tile) and t / 4 + 8.  Eight threads share a column pair, so a value that
+// belongs to a column is needed by 4 of a thread's rows at once.
+template <int OFF, int N>
+__device__ __forceinline__ void tmem_ld_frag8(uint32_t taddr, uint32_t (&r)[N]) {   // 64 columns
+  static_assert(OFF + 32 <= N, "register window out of range");
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[OFF + 0]), "=r"(r[OFF + 1]), "=r"(r[OFF + 2]), "=r"(r[OFF + 3]), "=r"(r[OFF + 4]), "=r"(r[OFF + 5]),
+        "=r"(r[OFF + 6]), "=r"(r[OFF + 7]), "=r"(r[OFF + 8]), "=r"(r[OFF + 9]), "=r"(r[OFF + 10]), "=r"(r[OFF + 11]),
+        "=r"(r[OFF + 12]), "=r"(r[OFF + 13]), "=r"(r[OFF + 14]), "=r"(r[OFF + 15]), "=r"(r[OFF + 16]),
+        "=r"(r[OFF + 17]), "=r"(r[OFF + 18]), "=r"(r[OFF + 19]), "=r"(r[OFF + 20]), "=r"(r[OFF + 21]),
+        "=r"(r[OFF + 22]), "=r"(r[OFF + 23]), "=r"(r[OFF + 24]), "=r"(r[OFF + 25]), "=r"(r[OFF + 26]),
+        "=r"(r[OFF + 27]), "=r"(r[OFF + 28]), "=r"(r[OFF + 29]), "=r"(r[OFF + 30]), "=r"(r[OFF + 31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_frag4(uint32_t taddr, uint32_t (&r)[16]) {   // 32 columns
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// The same tiles with each column pair packed to one 32-bit column (4 columns a tile): one
+// register for row t / 4, one for t / 4 + 8.
+__device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t (&r)[8]) {   // 16 columns
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t lds64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // slabs with real tokens of the tiles at temporal index t
 __device__ __forceinline__ int32_t slabs_at(const DiffGeo& g, int32_t t) { return t == g.nT - 1 ? g.slabs_last : g.slabs; }
 
@@ -113,6 +158,33 @@ __device__ __forceinline__ void next_block(const DiffGeo& g, const Item& it, Blo
   b.h = it.bh0;
   ++b.t;
 }
+// The blocks of an item's box in order, for roles that only need them to mask pads; empty otherwise.
+template <bool PAD>
+struct Walk {
+  __device__ __forceinline__ void start(const Item&) {}
+  __device__ __forceinline__ void next(const DiffGeo&) {}
+};
+template <>
+struct Walk<true> {
+  Block b;
+  int32_t h0, h1, w0, w1;
+  __device__ __forceinline__ void start(const Item& it) {
+    b = first_block(it);
+    h0 = it.bh0;
+    h1 = h0 + it.enh;
+    w0 = it.bw0;
+    w1 = w0 + it.enw;
+  }
+  __device__ __forceinline__ void next(const DiffGeo& g) {
+    if (++b.s < slabs_at(g, b.t)) return;
+    b.s = 0;
+    if (++b.w < w1) return;
+    b.w = w0;
+    if (++b.h < h1) return;
+    b.h = h0;
+    ++b.t;
+  }
+};
 // First row of a block in the tiled order of the padded latent.
 __device__ __forceinline__ int32_t tiled_row(const DiffGeo& g, const Block& b) {
   return ((b.t * g.nH + b.h) * g.nW + b.w) * g.ntile + b.s * kBlockRows;
@@ -160,9 +232,60 @@ __device__ __forceinline__ void load_block(const DiffGeo& g, uint32_t dst, const
   }
 }
 
-// Byte offset (>> 4) of K16 slice k16 in a 128-row K-major block of 64-column boxes.
-__device__ __forceinline__ uint64_t koff(int k16) {
-  return static_cast<uint64_t>(((k16 >> 2) * 16384 + (k16 & 3) * 32) >> 4);
+// Calls f(Const<0>), f(Const<1>), ... f(Const<N - 1>): an unrolled loop whose index is a constant.
+template <int I>
+struct Const {
+  static constexpr int value = I;
+};
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(Const<I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
+// Shared-memory matrix descriptors (128-byte swizzle, 1024 bytes between 8-row groups)
+// differ in their low word only: address >> 4, and the leading byte offset >> 4 above it.
+// An issuing thread keeps one low word per operand; the offset of a K16 slice is added
+// inside the instruction's own asm.  (As 64-bit values made outside, the slices of every
+// operand are hoisted out of the block loop and spill: the dK, dV kernel then waited for
+// local loads between its MMAs.)
+constexpr uint32_t kDescHi = 0x40004040u;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+constexpr uint32_t kLboK = 16;                  // K-major operands
+constexpr uint32_t kLboMn = kBlockRows * 128;   // MN-major: 64-column boxes
+
+// Offset (>> 4) of K16 slice k16 in a 128-row K-major block of 64-column boxes.
+constexpr uint32_t koff(int k16) { return static_cast<uint32_t>(((k16 >> 2) * 16384 + (k16 & 3) * 32) >> 4); }
+// ... of K16 slice k16 (16 rows) of an MN-major block
+constexpr uint32_t mnoff(int k16) { return static_cast<uint32_t>(k16 * (2048 >> 4)); }
+
+template <uint32_t AO, uint32_t BO>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 u, v;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 x, %1, %5;\n\t"
+      "add.u32 y, %2, %6;\n\t"
+      "mov.b64 u, {x, %7};\n\t"
+      "mov.b64 v, {y, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], u, v, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(AO), "n"(BO), "n"(kDescHi)
+      : "memory");
+}
+// A from tensor memory, AO columns further
+template <uint32_t AO, uint32_t BO>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 v;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 x, %1, %5;\n\t"
+      "add.u32 y, %2, %6;\n\t"
+      "mov.b64 v, {y, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], v, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(AO), "n"(BO), "n"(kDescHi)
+      : "memory");
 }
 
 // ---------------------------------------------------------------- host side
