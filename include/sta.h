@@ -396,7 +396,7 @@ typedef enum { STA_BF16 = 0, STA_FP16 = 1, STA_FP32 = 2 } sta_dtype;
  *   rng: device int64[2], seed and offset, read by the kernel (a captured graph
  *     takes the values it finds there at each replay).
  * Every pointer to an array with `cols` columns is 16-byte aligned, whatever cols
- * is.  1 <= cols <= 16384.  rows = 0 is a no-op.  Outputs must not overlap inputs or
+ * is.  1 <= cols <= 8192.  rows = 0 is a no-op.  Outputs must not overlap inputs or
  * one another.
  * Errors: NULL, ALIGN, ALIAS, SHAPE, ARG, ARCH, CUDA.
  */

@@ -571,7 +571,18 @@ def _forward_from_host_chunks(q_h, k_h, v_h, out_h, grid, tile, window_per_head,
     s_run.synchronize()
 
 
-from .block import (sta_diff_attention_bwd, sta_diff_attention_bwd_workspace, sta_diff_attention_fwd,  # noqa: E402
-                    sta_diff_attention_fwd_workspace, sta_diff_forward, sta_dropout, sta_dropout_forward,
-                    sta_layer_norm_backward, sta_layer_norm_bwd, sta_layer_norm_bwd_workspace, sta_layer_norm_forward,
-                    sta_layer_norm_fwd)
+# The operators around an attention block (block.py) are reached through the package too;
+# they are imported on first use, since that module needs torch at import.
+_BLOCK = frozenset((
+    "sta_diff_attention_bwd", "sta_diff_attention_bwd_workspace", "sta_diff_attention_fwd",
+    "sta_diff_attention_fwd_workspace", "sta_diff_forward", "sta_dropout", "sta_dropout_forward",
+    "sta_layer_norm_backward", "sta_layer_norm_bwd", "sta_layer_norm_bwd_workspace", "sta_layer_norm_forward",
+    "sta_layer_norm_fwd"))
+
+
+def __getattr__(name):
+    if name in _BLOCK:
+        from . import block
+        value = globals()[name] = getattr(block, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -11,25 +11,27 @@ the kernels are launched there, on ``stream`` or that device's current stream.
 from __future__ import annotations
 
 import contextlib
+import functools
 import math
 from typing import Optional, Sequence
 
-import numpy as np
+import torch
 
 from . import StaError, _check, _d3, _stream, _stream_context, _windows, load_library
 
 
+_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # sta_dtype
+
+
 def _dtype_code(dtype, name: str) -> int:
-    import torch
-    codes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    if dtype not in codes:
+    code = _CODES.get(dtype)
+    if code is None:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
-    return codes[dtype]
+    return code
 
 
 def _ptr(x, name: str, dtype=None, shape=None, optional: bool = False) -> Optional[int]:
     """Address of a contiguous CUDA tensor, checked against ``dtype`` and ``shape``."""
-    import torch
     if x is None and optional:
         return None
     if not isinstance(x, torch.Tensor):
@@ -38,26 +40,49 @@ def _ptr(x, name: str, dtype=None, shape=None, optional: bool = False) -> Option
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if shape is not None and tuple(x.shape) != tuple(shape):
+    if shape is not None and x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return x.data_ptr()
 
 
-@contextlib.contextmanager
-def _on(stream, *tensors):
-    """Runs the body on the tensors' device (they must share one) and on ``stream``;
-    yields the raw stream handle."""
-    import torch
-    devices = {t.device for t in tensors if isinstance(t, torch.Tensor)}
-    if len(devices) > 1:
-        raise ValueError(f"tensors of one call must be on one device, got {sorted(str(d) for d in devices)}")
-    dev = next(iter(devices), None)
-    if dev is None or dev.type != "cuda":
-        raise ValueError("CUDA tensors are required")
-    with torch.cuda.device(dev), _stream_context(stream):
-        yield _stream(stream)
+class _On:
+    """Runs the body on the tensors' device (they must share one) and on ``stream``; yields
+    the raw stream handle.  Where both are current already, nothing is switched."""
+
+    __slots__ = ("stream", "tensors", "stack")
+
+    def __init__(self, stream, *tensors):
+        for t in tensors:
+            if t is not None and not isinstance(t, torch.Tensor):
+                raise TypeError(f"expected a torch.Tensor, got {type(t).__name__}")
+        self.stream, self.tensors, self.stack = stream, tensors, None
+
+    def __enter__(self):
+        dev = None
+        for t in self.tensors:
+            if t is not None:
+                d = t.device
+                if dev is None:
+                    dev = d
+                elif d != dev:
+                    raise ValueError(f"tensors of one call must be on one device, got {dev} and {d}")
+        if dev is None or dev.type != "cuda":
+            raise ValueError("CUDA tensors are required")
+        if self.stream is None and dev.index == torch.cuda.current_device():
+            return torch._C._cuda_getCurrentRawStream(dev.index)
+        with contextlib.ExitStack() as stack:
+            stack.enter_context(torch.cuda.device(dev))
+            stack.enter_context(_stream_context(self.stream))
+            raw = _stream(self.stream)
+            self.stack = stack.pop_all()
+        return raw
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            return self.stack.__exit__(*exc)
+        return False
 
 
 def _workspace_ptr(ws, name: str):
@@ -65,6 +90,16 @@ def _workspace_ptr(ws, name: str):
     if ws is None:
         return None, 0
     return _ptr(ws, name), ws.numel() * ws.element_size()
+
+
+@functools.lru_cache(maxsize=64)
+def _geometry_args(grid, tile, windows):
+    """The C arguments of a (grid, tile, windows) triple; built once for each value."""
+    return _d3(grid), _d3(tile), _windows(windows)
+
+
+def _geometry(grid, tile, windows):
+    return _geometry_args(tuple(grid), tuple(tile), tuple(map(tuple, windows)))
 
 
 # ------------------------------------------------------------------ layer norm and dropout
@@ -78,18 +113,13 @@ def _rows_cols(x, name: str):
 
 def _params(weight, bias, cols: int, dtype):
     """Pointers of the weight and the bias and the code of their element type."""
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _ptr(t, name, shape=(cols,))
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise TypeError(f"weight and bias types differ: {weight.dtype}, {bias.dtype}")
     pd = weight.dtype if weight is not None else (bias.dtype if bias is not None else dtype)
-    return (None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
-            _dtype_code(pd, "weight"))
+    return (_ptr(weight, "weight", None, (cols,), True), _ptr(bias, "bias", None, (cols,), True), _dtype_code(pd, "weight"))
 
 
 def _rng_ptr(rng):
-    import torch
     return _ptr(rng, "rng", torch.int64, (2,), optional=True)
 
 
@@ -99,10 +129,9 @@ def sta_layer_norm_fwd(x, weight, bias, y, eps: float = 1e-5, residual=None, h=N
     CUDA tensors (bf16, fp16 or fp32; weight and bias of the same type or fp32, each may
     be None).  ``h`` receives the sum, ``mean`` and ``rstd`` (fp32 [rows]) the row
     statistics.  ``rng``: int64 CUDA tensor [seed, offset], needed when ``dropout_p`` > 0."""
-    import torch
     rows, cols = _rows_cols(x, "x")
     code = _dtype_code(x.dtype, "x")
-    with _on(stream, x, weight, bias, y, residual, h, mean, rstd, rng) as st:
+    with _On(stream, x, weight, bias, y, residual, h, mean, rstd, rng) as st:
         w, b, pcode = _params(weight, bias, cols, x.dtype)
         px = _ptr(x, "x")
         py = _ptr(y, "y", x.dtype, x.shape)
@@ -118,9 +147,8 @@ def sta_layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, residua
                            rng=None, stream=None):
     """``sta_layer_norm_fwd`` into new tensors: (y, h, mean, rstd).  ``h`` is None where
     it would be x itself (no residual and no dropout)."""
-    import torch
     rows, _ = _rows_cols(x, "x")
-    with _on(stream, x):
+    with _On(stream, x):
         y = torch.empty_like(x)
         h = torch.empty_like(x) if residual is not None or dropout_p > 0 else None
         mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
@@ -142,10 +170,9 @@ def sta_layer_norm_bwd(dy, h, mean, rstd, weight, dx=None, dresidual=None, dweig
     residual stream), ``dx`` that gradient through the dropout mask; ``dweight`` and
     ``dbias`` are sums over the rows.  ``workspace`` (a CUDA tensor of at least
     ``sta_layer_norm_bwd_workspace`` bytes) is allocated when it is None."""
-    import torch
     rows, cols = _rows_cols(h, "h")
     code = _dtype_code(h.dtype, "h")
-    with _on(stream, dy, h, mean, rstd, weight, dx, dresidual, dweight, dbias, dh, rng, workspace) as st:
+    with _On(stream, dy, h, mean, rstd, weight, dx, dresidual, dweight, dbias, dh, rng, workspace) as st:
         if workspace is None and (dweight is not None or dbias is not None):
             workspace = torch.empty(sta_layer_norm_bwd_workspace(rows, cols), dtype=torch.uint8, device=h.device)
         w, _, pcode = _params(weight, None, cols, h.dtype)
@@ -168,8 +195,7 @@ def sta_layer_norm_backward(dy, h, mean, rstd, weight=None, dh=None, bias: bool 
     """``sta_layer_norm_bwd`` into new tensors: (dx, dresidual, dweight, dbias).  Without
     dropout dresidual is dx itself; dweight is None without a weight, dbias without
     ``bias``.  Both have the weight's type (h's type without a weight)."""
-    import torch
-    with _on(stream, h):
+    with _On(stream, h):
         dx = torch.empty_like(h)
         dres = torch.empty_like(h) if dropout_p > 0 else None
         pd = h.dtype if weight is None else weight.dtype
@@ -186,15 +212,14 @@ def sta_dropout(x, y, dropout_p: float, rng, stream=None) -> None:
     [seed, offset]) and the element's place; call it on the gradient with the same rng
     for the backward."""
     rows, cols = _rows_cols(x, "x")
-    with _on(stream, x, y, rng) as st:
+    with _On(stream, x, y, rng) as st:
         _check(load_library().sta_dropout(_ptr(x, "x"), _ptr(y, "y", x.dtype, x.shape), rows, cols,
                                           _dtype_code(x.dtype, "x"), float(dropout_p), _rng_ptr(rng), st), "sta_dropout")
 
 
 def sta_dropout_forward(x, dropout_p: float, rng, stream=None):
     """``sta_dropout`` into a new tensor."""
-    import torch
-    with _on(stream, x):
+    with _On(stream, x):
         y = torch.empty_like(x)
     sta_dropout(x, y, dropout_p, rng, stream)
     return y
@@ -205,9 +230,9 @@ def sta_dropout_forward(x, dropout_p: float, rng, stream=None):
 def _diff_dims(q, grid, token_major: bool, windows):
     if q.dim() != 4:
         raise ValueError("q must be [batch, heads, L, d], or [batch, L, heads, d] with token_major")
-    a, b, c, d = (int(x) for x in q.shape)
+    a, b, c, d = q.shape
     B, Hn, L = (a, c, b) if token_major else (a, b, c)
-    if L != int(np.prod([int(x) for x in grid])):
+    if L != grid[0] * grid[1] * grid[2]:
         raise ValueError("L must equal T*H*W")
     if len(windows) != Hn:
         raise ValueError("one window per head is required")
@@ -216,7 +241,7 @@ def _diff_dims(q, grid, token_major: bool, windows):
 
 def _diff_workspace(which: str, q, grid, tile, windows, token_major: bool) -> int:
     B, Hn, _, d = _diff_dims(q, grid, token_major, windows)
-    n = getattr(load_library(), which)(B, Hn, d, _d3(grid), _d3(tile), _windows(windows))
+    n = getattr(load_library(), which)(B, Hn, d, *_geometry(grid, tile, windows))
     if n < 0:
         raise StaError(10, which)
     return int(n)
@@ -242,9 +267,9 @@ def sta_diff_attention_fwd(q, k, v, lam, out, grid, tile, window_per_head: Seque
     [2, B, heads, L]) both maps' log-sum-exps, which the backward needs.
     ``workspace`` (at least ``sta_diff_attention_fwd_workspace`` bytes) is allocated
     when it is None."""
-    import torch
     B, Hn, L, d = _diff_dims(q, grid, token_major, window_per_head)
-    with _on(stream, q, k, v, lam, out, out2, lse, workspace) as st:
+    geo = _geometry(grid, tile, window_per_head)
+    with _On(stream, q, k, v, lam, out, out2, lse, workspace) as st:
         shape = q.shape
         ptrs = [_ptr(q, "q", torch.bfloat16)] + [_ptr(t, n, torch.bfloat16, shape) for n, t in (("k", k), ("v", v))]
         ptrs.append(_ptr(lam, "lam", torch.float32, (Hn,)))
@@ -252,12 +277,12 @@ def sta_diff_attention_fwd(q, k, v, lam, out, grid, tile, window_per_head: Seque
         ptrs.append(_ptr(out2, "out2", torch.bfloat16, shape, optional=True))
         ptrs.append(_ptr(lse, "lse", torch.float32, (2, B, Hn, L), optional=True))
         if workspace is None:
-            need = load_library().sta_diff_attention_fwd_workspace(B, Hn, d, _d3(grid), _d3(tile), _windows(window_per_head))
+            need = load_library().sta_diff_attention_fwd_workspace(B, Hn, d, *geo)
             if need > 0:
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         pw, nw = _workspace_ptr(workspace, "workspace")
-        _check(load_library().sta_diff_attention_fwd(*ptrs, B, Hn, d, int(bool(token_major)), _d3(grid), _d3(tile),
-                                                     _windows(window_per_head), float(scale), pw, nw, st),
+        _check(load_library().sta_diff_attention_fwd(*ptrs, B, Hn, d, int(bool(token_major)), *geo, float(scale), pw, nw,
+                                                     st),
                "sta_diff_attention_fwd")
 
 
@@ -267,21 +292,21 @@ def sta_diff_attention_bwd(q, k, v, lam, out, out2, lse, dout, dq, dk, dv, dlam,
     and dlam (fp32 [heads]) from the forward's inputs, out, out2, lse and the output
     gradient dout.  ``workspace`` (at least ``sta_diff_attention_bwd_workspace`` bytes)
     is allocated when it is None."""
-    import torch
     B, Hn, L, d = _diff_dims(q, grid, token_major, window_per_head)
-    with _on(stream, q, k, v, lam, out, out2, lse, dout, dq, dk, dv, dlam, workspace) as st:
+    geo = _geometry(grid, tile, window_per_head)
+    with _On(stream, q, k, v, lam, out, out2, lse, dout, dq, dk, dv, dlam, workspace) as st:
         shape = q.shape
         bf = lambda t, n: _ptr(t, n, torch.bfloat16, shape)  # noqa: E731
         ptrs = [bf(q, "q"), bf(k, "k"), bf(v, "v"), _ptr(lam, "lam", torch.float32, (Hn,)), bf(out, "out"),
                 bf(out2, "out2"), _ptr(lse, "lse", torch.float32, (2, B, Hn, L)), bf(dout, "dout"), bf(dq, "dq"),
                 bf(dk, "dk"), bf(dv, "dv"), _ptr(dlam, "dlam", torch.float32, (Hn,))]
         if workspace is None:
-            need = load_library().sta_diff_attention_bwd_workspace(B, Hn, d, _d3(grid), _d3(tile), _windows(window_per_head))
+            need = load_library().sta_diff_attention_bwd_workspace(B, Hn, d, *geo)
             if need > 0:
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         pw, nw = _workspace_ptr(workspace, "workspace")
-        _check(load_library().sta_diff_attention_bwd(*ptrs, B, Hn, d, int(bool(token_major)), _d3(grid), _d3(tile),
-                                                     _windows(window_per_head), float(scale), pw, nw, st),
+        _check(load_library().sta_diff_attention_bwd(*ptrs, B, Hn, d, int(bool(token_major)), *geo, float(scale), pw, nw,
+                                                     st),
                "sta_diff_attention_bwd")
 
 
@@ -290,10 +315,9 @@ def sta_diff_forward(q, k, v, lam, grid, tile, window_per_head: Sequence, scale:
     """``sta_diff_attention_fwd`` into new tensors, allocated on ``stream``: out, or
     (out, out2, lse) with ``save`` (what the backward needs).  ``scale`` defaults to
     1 / sqrt(d / 2), d / 2 being the columns of one map."""
-    import torch
     B, Hn, L, d = _diff_dims(q, grid, token_major, window_per_head)
     sc = 1.0 / math.sqrt(d / 2) if scale is None else float(scale)
-    with _on(stream, q):
+    with _On(stream, q):
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         out2 = torch.empty_like(out) if save else None
         lse = torch.empty((2, B, Hn, L), dtype=torch.float32, device=q.device) if save else None

@@ -15,160 +15,417 @@ namespace {
 
 using namespace norm;
 
-// TPR threads share a row (0: the whole block); each holds CH chunks of R rows.
-template <typename T, bool VEC, int TPR, int CH, int R>
+// TPR threads share a row (0: the whole block); a thread holds CH chunks of R rows at a
+// time.  A warp (or block) takes consecutive rows; STAGES - 1 of its steps are on their way
+// to shared memory while one is in registers, so the bytes in flight do not depend on the
+// registers: with the next rows prefetched into registers the kernel moved 3.8 TB/s.
+template <typename T, int TPR, int CH, int R, int STAGES>
 __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const NormFwdArgs a) {
-  __shared__ float red[32];
-  const int lane = TPR > 0 ? static_cast<int>(threadIdx.x) % TPR : static_cast<int>(threadIdx.x);
-  const int step = TPR > 0 ? TPR : static_cast<int>(blockDim.x);
-  const int64_t group = TPR > 0 ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / TPR) + threadIdx.x / TPR : blockIdx.x;
-  const int64_t row0 = group * R;
+  constexpr bool VEC = false;
+  constexpr bool kBlock = TPR == 0;
+  constexpr bool kKeep = CH <= 2 && !kBlock;      // weight and bias stay in registers
+  constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
+  constexpr int kRows = kGroups * R;              // rows of a step
+  __shared__ float red[2][R][32];   // block mode: sums of a row, of its values and of its squares
+  extern __shared__ __align__(16) uint8_t bufs[];
+  const int lane = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x & 31) % (TPR > 0 ? TPR : 1);
+  const int grp = kBlock ? 0 : static_cast<int>(threadIdx.x & 31) / (TPR > 0 ? TPR : 1);
+  const int step = kBlock ? static_cast<int>(blockDim.x) : TPR;
+  const int st = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x & 31);
+  const int snt = kBlock ? static_cast<int>(blockDim.x) : 32;
+  const int64_t unit = kBlock ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t units = kBlock ? gridDim.x : static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   const int32_t n8 = (a.cols + 7) >> 3;
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.residual);
+  T* y = static_cast<T*>(a.y);
+  T* h = static_cast<T*>(a.h);
   PhiloxKey key{};
   if (a.drop.thr > 0) key = philox_key(a.drop.rng);
-  float f[R][CH][8];
-  {
-    Chunk<T> cx[R][CH], cr[R][CH];
+  const float inv_n = 1.0f / static_cast<float>(a.cols);
+  const uint32_t one = span_bytes<T>(static_cast<uint32_t>(kRows) * a.cols), stage = res != nullptr ? 2 * one : one;
+  uint8_t* mine = bufs + (kBlock ? 0 : (threadIdx.x >> 5) * STAGES * stage);
+  uint64_t w[kKeep ? CH : 1][4], b[kKeep ? CH : 1][4];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int32_t ch = lane + k * step;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[k][i] = both(1.f);
+        b[k][i] = 0;
+      }
+      if (ch < n8) {
+        const int n = VEC ? 8 : min(8, a.cols - ch * 8);
+        if (a.weight != nullptr) load_param2<T, VEC>(a.weight, a.wfp32, ch * 8, n, w[k]);
+        if (a.bias != nullptr) load_param2<T, VEC>(a.bias, a.wfp32, ch * 8, n, b[k]);
+      }
+    }
+  }
+  auto rows_at = [&](int64_t base) { return static_cast<int>(min(static_cast<int64_t>(kRows), a.rows - base)); };
+  auto fetch = [&](int64_t base, int slot) {   // the step that starts at row `base`, if there is one
+    if (base < a.rows) {
+      const int n = rows_at(base) * a.cols;
+      uint8_t* p = mine + slot * stage;
+      span_load(p, x + base * a.cols, n, st, snt);
+      if (res != nullptr) span_load(p + one, res + base * a.cols, n, st, snt);
+    }
+    span_commit();
+  };
+  int64_t ahead = unit * kRows;
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i, ahead += units * kRows) fetch(ahead, i);
+  int slot = 0;
+  for (int64_t base = unit * kRows; base < a.rows; base += units * kRows, ahead += units * kRows) {
+    fetch(ahead, slot == 0 ? STAGES - 1 : slot - 1);
+    span_wait<STAGES - 1>();
+    span_sync<kBlock>();
+    const int live = rows_at(base);
+    uint8_t* p = mine + slot * stage;
+    uint64_t f[R][CH][4];
+    const T* ex = span_elems(p, x + base * a.cols);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        const int32_t ch = lane + k * step;
-        const int n = VEC ? 8 : min(8, a.cols - ch * 8);
-        cx[r][k].clear();
-        if (row0 + r < a.rows && ch < n8) {
-          const int64_t at = (row0 + r) * a.cols + ch * 8;
-          if (VEC) cx[r][k].load(x + at); else cx[r][k].load_n(x + at, n);
-        }
+        const int q = r * kGroups + grp, c0 = (lane + k * step) * 8;
+        span_get<T, VEC>(ex, q * a.cols + c0, q < live ? a.cols - c0 : 0, f[r][k]);
       }
+    if (a.drop.thr > 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+          drop_pairs(f[r][k], static_cast<uint64_t>(base + r * kGroups + grp) * n8 + (lane + k * step), key, a.drop);
+    }
     if (res != nullptr) {
+      const T* er = span_elems(p + one, res + base * a.cols);
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-          const int32_t ch = lane + k * step;
-          const int n = VEC ? 8 : min(8, a.cols - ch * 8);
-          cr[r][k].clear();
-          if (row0 + r < a.rows && ch < n8) {
-            const int64_t at = (row0 + r) * a.cols + ch * 8;
-            if (VEC) cr[r][k].load(res + at); else cr[r][k].load_n(res + at, n);
-          }
+          const int q = r * kGroups + grp, c0 = (lane + k * step) * 8;
+          uint64_t g[4];
+          span_get<T, VEC>(er, q * a.cols + c0, q < live ? a.cols - c0 : 0, g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[r][k][i] = add_f32x2(f[r][k][i], g[i]);
         }
     }
+    float mean[R], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      uint64_t s[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i & 1] = add_f32x2(s[i & 1], f[r][k][i]);   // columns past the row hold zero
+      mean[r] = row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[0][r]) * inv_n;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t nm = both(-mean[r]);
+      uint64_t s[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int32_t left = a.cols - (lane + k * step) * 8;   // columns of the chunk that exist
+        if (VEC ? left > 0 : left >= 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t e = add_f32x2(f[r][k][i], nm);
+            s[i & 1] = fma_f32x2(e, e, s[i & 1]);
+          }
+        } else if (!VEC) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float u, v;
+            f32x2_split(add_f32x2(f[r][k][i], nm), u, v);
+            const uint64_t e = f32x2(2 * i < left ? u : 0.f, 2 * i + 1 < left ? v : 0.f);
+            s[i & 1] = fma_f32x2(e, e, s[i & 1]);
+          }
+        }
+      }
+      rstd[r] = rsqrtf(fmaf(row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[1][r]), inv_n, a.eps));
+    }
+    // rows out: h as it is, y normalised
+#pragma unroll
+    for (int out = 0; out < 2; ++out) {
+      T* dst = out == 0 ? h : y;
+      if (dst == nullptr) continue;
+      if (!VEC) span_sync<kBlock>();   // the slot's values are in registers (or stored): it carries the output
+      T* eo = span_elems(p, dst + base * a.cols);
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int32_t ch = lane + k * step;
+        if (ch >= n8) continue;
+        const int n = VEC ? 8 : min(8, a.cols - ch * 8);
+        uint64_t wk[4], bk[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          wk[i] = kKeep ? w[kKeep ? k : 0][i] : both(1.f);
+          bk[i] = kKeep ? b[kKeep ? k : 0][i] : 0;
+        }
+        if (!kKeep && out == 1) {
+          if (a.weight != nullptr) load_param2<T, VEC>(a.weight, a.wfp32, ch * 8, n, wk);
+          if (a.bias != nullptr) load_param2<T, VEC>(a.bias, a.wfp32, ch * 8, n, bk);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int q = r * kGroups + grp;
+          if (q >= live) continue;
+          uint64_t v[4];
+          const uint64_t nm = both(-mean[r]), rs = both(rstd[r]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = out == 0 ? f[r][k][i] : fma_f32x2(mul_f32x2(add_f32x2(f[r][k][i], nm), rs), wk[i], bk[i]);
+          if constexpr (VEC) {
+            Chunk<T> o;
+            o.put2(v);
+            o.store(dst + (base + q) * a.cols + ch * 8);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float u, t;
+              f32x2_split(v[i], u, t);
+              if (2 * i < n) eo[q * a.cols + ch * 8 + 2 * i] = from_f<T>(u);
+              if (2 * i + 1 < n) eo[q * a.cols + ch * 8 + 2 * i + 1] = from_f<T>(t);
+            }
+          }
+        }
+      }
+      if (!VEC) {
+        span_sync<kBlock>();
+        span_store(p, dst + base * a.cols, live * a.cols, st, snt);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int q = r * kGroups + grp;
+      if (lane == 0 && q < live) {
+        if (a.mean != nullptr) a.mean[base + q] = mean[r];
+        if (a.rstd != nullptr) a.rstd[base + q] = rstd[r];
+      }
+    }
+    span_sync<kBlock>();   // every thread is done with the slot: the next step's fetch fills it
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+  }
+  span_wait<0>();
+}
+
+// The same for rows of a multiple of eight columns (see Own): no shared spans, addresses
+// that advance by one constant, half the instructions.
+// DROP: with dropout, whose generator takes registers that the other calls use for more warps.
+template <typename T, bool DROP, int TPR, int CH, int R, int STAGES>
+__global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 ? 2 : 1) norm_fwd_vec_kernel(const NormFwdArgs a) {
+  constexpr bool kBlock = TPR == 0;
+  constexpr bool kKeep = CH <= 2 && !kBlock;      // weight and bias stay in registers
+  constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
+  constexpr int kRows = kGroups * R;              // rows of a step
+  constexpr int kParts = Own<T>::kParts;
+  constexpr int kChunkBytes = 16 * kParts;
+  __shared__ float red[2][R][32];   // block mode: sums of a row, of its values and of its squares
+  extern __shared__ __align__(16) uint8_t bufs[];
+  const int lane = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x & 31) % (TPR > 0 ? TPR : 1);
+  const int grp = kBlock ? 0 : static_cast<int>(threadIdx.x & 31) / (TPR > 0 ? TPR : 1);
+  const int step = kBlock ? static_cast<int>(blockDim.x) : TPR;
+  const uint32_t part = 16u * (kBlock ? blockDim.x : 256u);   // 16 bytes of every thread
+  const int64_t unit = kBlock ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t units = kBlock ? gridDim.x : static_cast<int64_t>(gridDim.x) * 8;
+  const int32_t n8 = a.cols >> 3;
+  const bool has_res = a.residual != nullptr;
+  const uint32_t arr = static_cast<uint32_t>(R * CH * kParts) * part;   // one array of one stage
+  const uint32_t stage = has_res ? 2 * arr : arr;
+  const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(bufs)) + 16 * threadIdx.x;
+  PhiloxKey key{};
+  if (DROP) key = philox_key(a.drop.rng);
+  const float inv_n = 1.0f / static_cast<float>(a.cols);
+  uint64_t w[kKeep ? CH : 1][4], b[kKeep ? CH : 1][4];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int32_t ch = lane + k * step;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[k][i] = both(1.f);
+        b[k][i] = 0;
+      }
+      if (ch < n8) {
+        if (a.weight != nullptr) load_param2<T, true>(a.weight, a.wfp32, ch * 8, 8, w[k]);
+        if (a.bias != nullptr) load_param2<T, true>(a.bias, a.wfp32, ch * 8, 8, b[k]);
+      }
+    }
+  }
+  // Addresses: one pointer per array, at this thread's first chunk of a step's first row; a
+  // step, a row of the step and a chunk each add a constant.  Rows are counted down from
+  // the thread's first one in 32 bits (capped where it cannot matter).
+  const int64_t row_bytes = static_cast<int64_t>(a.cols) * sizeof(T);
+  const int64_t step_bytes = units * kRows * row_bytes, r_bytes = kGroups * row_bytes;
+  const int k_bytes = step * kChunkBytes;
+  const int64_t row0 = unit * kRows + grp, off0 = row0 * row_bytes + lane * kChunkBytes;
+  const int64_t step_rows = units * kRows;
+  const int psize = a.wfp32 ? 4 : static_cast<int>(sizeof(T)), p_bytes = step * 8 * psize;
+  const char *wp = static_cast<const char*>(a.weight) + lane * 8 * psize, *bp = static_cast<const char*>(a.bias) + lane * 8 * psize;
+  const char* px = static_cast<const char*>(a.x) + off0;
+  const char* pr = static_cast<const char*>(a.residual) + off0;
+  int64_t left_in = a.rows - row0;
+  auto fetch = [&](uint32_t at) {
+    const int left = static_cast<int>(left_in < 4096 ? left_in : 4096);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        const int32_t ch = lane + k * step;
-        cx[r][k].get(f[r][k]);
-        if (a.drop.thr > 0) {
-          // dropped values are replaced, not multiplied by zero: an infinity or NaN there stays out
-          const uint32_t keep = philox_keep(philox_block(static_cast<uint64_t>(row0 + r) * n8 + ch, key), a.drop.thr);
+        // what does not exist reads as zero
+        const bool ok = r * kGroups < left && lane + k * step < n8;
+        const int64_t o = ok ? r * r_bytes + k * k_bytes : 0;
+        const uint32_t d = at + static_cast<uint32_t>((r * CH + k) * kParts) * part;
+        Own<T>::copy_or_zero(d, part, (ok ? px : static_cast<const char*>(a.x)) + o, ok);
+        if (has_res) Own<T>::copy_or_zero(d + arr, part, (ok ? pr : static_cast<const char*>(a.residual)) + o, ok);
+      }
+    span_commit();
+    left_in -= step_rows;
+    px += step_bytes;
+    pr += step_bytes;
+  };
+  const bool partial = n8 != step * CH;   // some threads have fewer chunks
+  int64_t row = row0, left64 = left_in;
+  char *py = static_cast<char*>(a.y) + off0, *ph = static_cast<char*>(a.h) + off0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[r][k][i] = (keep >> i) & 1u ? f[r][k][i] * a.drop.scale : 0.f;
-        }
-        if (res != nullptr) {
-          float g[8];
-          cr[r][k].get(g);
+  for (int i = 0; i < STAGES - 1; ++i) fetch(sm + i * stage);
+  uint32_t cur = 0;   // the stage in use
+  for (int64_t base = unit * kRows; base < a.rows; base += step_rows) {
+    const int left = static_cast<int>(left64 < 4096 ? left64 : 4096);
+    fetch(sm + (cur == 0 ? (STAGES - 1) * stage : cur - stage));
+    span_wait<STAGES - 1>();
+    uint64_t f[R][CH][4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[r][k][i] += g[i];
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const uint32_t d = sm + cur + static_cast<uint32_t>((r * CH + k) * kParts) * part;
+        Own<T>::read(d, part, f[r][k]);
+        if (DROP)
+          drop_pairs(f[r][k], static_cast<uint64_t>(row + r * kGroups) * n8 + (lane + k * step), key, a.drop);
+        if (has_res) {
+          uint64_t g[4];
+          Own<T>::read(d + arr, part, g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[r][k][i] = add_f32x2(f[r][k][i], g[i]);
         }
       }
-  }
-  const float inv_n = 1.0f / static_cast<float>(a.cols);
-  float mean[R], rstd[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += f[r][k][i];   // columns past the row hold zero
-    mean[r] = row_sum<TPR>(s, red) * inv_n;
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int32_t c0 = (lane + k * step) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = f[r][k][i] - mean[r];
-        if (c0 + (VEC ? 0 : i) < a.cols) s = fmaf(e, e, s);
-      }
-    }
-    rstd[r] = 1.0f / sqrtf(fmaf(row_sum<TPR>(s, red), inv_n, a.eps));
-  }
-  T* y = static_cast<T*>(a.y);
-  T* h = static_cast<T*>(a.h);
-#pragma unroll
-  for (int k = 0; k < CH; ++k) {
-    const int32_t ch = lane + k * step;
-    if (ch >= n8) continue;
-    const int n = VEC ? 8 : min(8, a.cols - ch * 8);
-    float w[8], b[8];
-    if (a.weight != nullptr) load_param<T, VEC>(a.weight, a.wfp32, ch * 8, n, w);
-    if (a.bias != nullptr) load_param<T, VEC>(a.bias, a.wfp32, ch * 8, n, b);
+    cur = cur + stage == STAGES * stage ? 0 : cur + stage;
+    float mean[R], rstd[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (row0 + r >= a.rows) continue;
-      const int64_t at = (row0 + r) * a.cols + ch * 8;
-      Chunk<T> o;
-      if (h != nullptr) {
-        o.put(f[r][k]);
-        if (VEC) o.store(h + at); else o.store_n(h + at, n);
-      }
-      float v[8];
+      uint64_t s[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = (f[r][k][i] - mean[r]) * rstd[r];
-        if (a.weight != nullptr) v[i] *= w[i];
-        if (a.bias != nullptr) v[i] += b[i];
-      }
-      o.put(v);
-      if (VEC) o.store(y + at); else o.store_n(y + at, n);
+      for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i & 1] = add_f32x2(s[i & 1], f[r][k][i]);   // missing chunks hold zero
+      mean[r] = row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[0][r]) * inv_n;
     }
+    if (a.h != nullptr) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+          if (r * kGroups < left && lane + k * step < n8) Own<T>::write(ph + r * r_bytes + k * k_bytes, f[r][k]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t nm = both(-mean[r]);
+      uint64_t s[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        if (partial && lane + k * step >= n8) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[r][k][i] = add_f32x2(f[r][k][i], nm);
+          s[i & 1] = fma_f32x2(f[r][k][i], f[r][k][i], s[i & 1]);
+        }
+      }
+      rstd[r] = rsqrtf(fmaf(row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[1][r]), inv_n, a.eps));
+    }
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int32_t ch = lane + k * step;
+      if (ch >= n8) continue;
+      uint64_t wk[4], bk[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        wk[i] = kKeep ? w[kKeep ? k : 0][i] : both(1.f);
+        bk[i] = kKeep ? b[kKeep ? k : 0][i] : 0;
+      }
+      if (!kKeep) {
+        if (a.weight != nullptr) read_param2<T>(wp + k * p_bytes, a.wfp32, wk);
+        if (a.bias != nullptr) read_param2<T>(bp + k * p_bytes, a.wfp32, bk);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint64_t rs = both(rstd[r]);
+        uint64_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fma_f32x2(mul_f32x2(f[r][k][i], rs), wk[i], bk[i]);
+        if (r * kGroups < left) Own<T>::write(py + r * r_bytes + k * k_bytes, v);
+      }
+    }
+    if (lane == 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r * kGroups < left) {
+          if (a.mean != nullptr) (a.mean + row)[r * kGroups] = mean[r];
+          if (a.rstd != nullptr) (a.rstd + row)[r * kGroups] = rstd[r];
+        }
+    }
+    left64 -= step_rows;
+    row += step_rows;
+    py += step_bytes;
+    ph += step_bytes;
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (lane == 0 && row0 + r < a.rows) {
-      if (a.mean != nullptr) a.mean[row0 + r] = mean[r];
-      if (a.rstd != nullptr) a.rstd[row0 + r] = rstd[r];
-    }
+  span_wait<0>();
 }
 
-template <typename T, bool VEC, int TPR, int CH, int R>
+template <typename T, bool VEC, int TPR, int CH, int R, int STAGES>
 cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t stream) {
+  void (*kern)(NormFwdArgs);
+  if constexpr (VEC)
+    kern = a.drop.thr > 0 ? norm_fwd_vec_kernel<T, true, TPR, CH, R, STAGES> : norm_fwd_vec_kernel<T, false, TPR, CH, R, STAGES>;
+  else
+    kern = norm_fwd_kernel<T, TPR, CH, R, STAGES>;
+  constexpr int rows = (TPR > 0 ? 32 / (TPR > 0 ? TPR : 1) : 1) * R;   // of a warp's (block's) step
   int threads = 256;
-  int64_t blocks;
-  if (TPR > 0) {
-    const int64_t groups = (a.rows + R - 1) / R, per = threads / TPR;
-    blocks = (groups + per - 1) / per;
-  } else {
-    const int n8 = (a.cols + 7) >> 3;
-    threads = ((n8 + CH - 1) / CH + 31) / 32 * 32;
-    blocks = (a.rows + R - 1) / R;
-  }
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  norm_fwd_kernel<T, VEC, (TPR > 0 ? TPR : 0), CH, R><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(a);
+  if (TPR == 0) threads = (((a.cols + 7) / 8 + CH - 1) / CH + 31) / 32 * 32;
+  const int per_block = (TPR > 0 ? threads / 32 : 1);
+  const int stage = VEC ? R * CH * threads * 8 * static_cast<int>(sizeof(T))
+                        : per_block * static_cast<int>(span_bytes<T>(static_cast<uint32_t>(rows) * a.cols));
+  const int smem = STAGES * (a.residual != nullptr ? 2 : 1) * stage;
+  int sms = 0, dev = 0, fit = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, threads, smem);
+  if (e != cudaSuccess) return e;
+  if (fit < 1) return cudaErrorInvalidConfiguration;
+  const int64_t need = ((a.rows + rows - 1) / rows + per_block - 1) / per_block;
+  const int64_t most = static_cast<int64_t>(sms) * fit;
+  kern<<<static_cast<unsigned>(need < most ? need : most), threads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
+// A warp takes rows of up to 1536 columns (48 values of a row in a thread's registers), a
+// block longer ones.  Short rows: two chunks a thread rather than one, which halves the
+// shuffles of a row's sums.
 template <typename T, bool VEC>
 cudaError_t pick_fwd(const NormFwdArgs& a, cudaStream_t stream) {
+  constexpr int S = sizeof(T) == 4 ? 2 : 4;   // 4 KB a stage, array and warp at most
   const int n8 = (a.cols + 7) >> 3;
-  if (n8 <= 1) return launch_fwd<T, VEC, 1, 1, 2>(a, stream);
-  if (n8 <= 4) return launch_fwd<T, VEC, 4, 1, 4>(a, stream);
-  if (n8 <= 16) return launch_fwd<T, VEC, 16, 1, 4>(a, stream);
-  if (n8 <= 32) return launch_fwd<T, VEC, 32, 1, 4>(a, stream);
-  if (n8 <= 64) return launch_fwd<T, VEC, 32, 2, 2>(a, stream);
-  if (n8 <= 128) return launch_fwd<T, VEC, 32, 4, 1>(a, stream);
-  if (n8 <= 192) return launch_fwd<T, VEC, 32, 6, 1>(a, stream);
-  if (n8 <= 1024) return launch_fwd<T, VEC, 0, 2, 1>(a, stream);
-  return launch_fwd<T, VEC, 0, 4, 1>(a, stream);
+  if (n8 <= 1) return launch_fwd<T, VEC, 1, 1, 2, S>(a, stream);
+  if (n8 <= 4) return launch_fwd<T, VEC, 2, 2, 2, S>(a, stream);
+  if (n8 <= 8) return launch_fwd<T, VEC, 4, 2, 2, S>(a, stream);
+  if (n8 <= 16) return launch_fwd<T, VEC, 8, 2, 2, S>(a, stream);
+  if (n8 <= 32) return launch_fwd<T, VEC, 16, 2, 2, S>(a, stream);
+  if (n8 <= 64) return launch_fwd<T, VEC, 32, 2, 2, S>(a, stream);
+  if (n8 <= 128) return launch_fwd<T, VEC, 32, 4, 1, 2>(a, stream);
+  if (n8 <= 192 && sizeof(T) == 2) return launch_fwd<T, VEC, 32, 6, 1, 2>(a, stream);
+  return launch_fwd<T, VEC, 0, 2, 1, 2>(a, stream);
 }
 
 // Dropout, rows of a multiple of eight columns: chunk i of the flat array is counter block i.

@@ -7,7 +7,7 @@
 
 namespace sta {
 
-constexpr int32_t kNormMaxCols = 16384;
+constexpr int32_t kNormMaxCols = 8192;
 
 struct NormDropout {
   const int64_t* rng;   // seed, offset on the device; null when thr is 0

@@ -43,125 +43,171 @@ __device__ __forceinline__ void row_sum2(float& u, float& v, float2* red) {
   }
 }
 
-template <typename T, bool VEC, int TPR, int CH, int R>
+// TPR threads share a row (0: the whole block); a thread holds CH chunks of R rows at a
+// time, while the next STAGES - 1 steps of its warp (block) are on their way to shared memory.
+template <typename T, int TPR, int CH, int R, int STAGES>
 __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const NormBwdArgs a) {
+  constexpr bool VEC = false;
+  constexpr bool kBlock = TPR == 0;
+  constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
+  constexpr int kRows = kGroups * R;   // rows of a warp's (block's) step
   // block mode: partial row sums, a buffer per row in flight and per step parity
   __shared__ float2 red[2][R][32];
-  const int lane = TPR > 0 ? static_cast<int>(threadIdx.x) % (TPR > 0 ? TPR : 1) : static_cast<int>(threadIdx.x);
-  const int step = TPR > 0 ? TPR : static_cast<int>(blockDim.x);
-  const int per_block = TPR > 0 ? 256 / (TPR > 0 ? TPR : 1) : 1;
-  const int my = TPR > 0 ? static_cast<int>(threadIdx.x) / (TPR > 0 ? TPR : 1) : 0;
+  extern __shared__ __align__(16) uint8_t bufs[];
+  const int lane = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x & 31) % (TPR > 0 ? TPR : 1);
+  const int grp = kBlock ? 0 : static_cast<int>(threadIdx.x & 31) / (TPR > 0 ? TPR : 1);
+  const int step = kBlock ? static_cast<int>(blockDim.x) : TPR;
+  const int st = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x & 31);
+  const int snt = kBlock ? static_cast<int>(blockDim.x) : 32;
+  const int64_t unit = kBlock ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t units = kBlock ? gridDim.x : static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   const int32_t n8 = (a.cols + 7) >> 3;
   const T* dy = static_cast<const T*>(a.dy);
   const T* h = static_cast<const T*>(a.h);
   const T* dh = static_cast<const T*>(a.dh);
-  T* dx = static_cast<T*>(a.dx);
-  T* dres = static_cast<T*>(a.dres);
   PhiloxKey key{};
   if (a.drop.thr > 0) key = philox_key(a.drop.rng);
-  float w[CH][8], dw[CH][8], db[CH][8];
+  const uint32_t one = span_bytes<T>(static_cast<uint32_t>(kRows) * a.cols), stage = (dh != nullptr ? 3 : 2) * one;
+  uint8_t* mine = bufs + (kBlock ? 0 : (threadIdx.x >> 5) * STAGES * stage);
+  uint64_t w[CH][4], dw[CH][4], db[CH][4];   // pairs of columns
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int32_t ch = lane + k * step;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[k][i] = 1.f;
-      dw[k][i] = 0.f;
-      db[k][i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      w[k][i] = both(1.f);
+      dw[k][i] = 0;
+      db[k][i] = 0;
     }
     if (a.weight != nullptr && ch < n8)
-      load_param<T, VEC>(a.weight, a.wfp32, ch * 8, VEC ? 8 : min(8, a.cols - ch * 8), w[k]);
+      load_param2<T, VEC>(a.weight, a.wfp32, ch * 8, VEC ? 8 : min(8, a.cols - ch * 8), w[k]);
   }
   const float inv_n = 1.0f / static_cast<float>(a.cols);
-  int par = 0;
-  // the block's rows: every thread makes the same number of steps (the sums synchronise)
-  for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * per_block * R; b0 < a.rows;
-       b0 += static_cast<int64_t>(gridDim.x) * per_block * R, par ^= 1) {
-    const int64_t row0 = b0 + static_cast<int64_t>(my) * R;
-    Chunk<T> cy[R][CH], cz[R][CH];
-    float mean[R], rstd[R];
+  auto rows_at = [&](int64_t base) { return static_cast<int>(min(static_cast<int64_t>(kRows), a.rows - base)); };
+  auto fetch = [&](int64_t base, int slot) {   // the step that starts at row `base`, if there is one
+    if (base < a.rows) {
+      const int n = rows_at(base) * a.cols;
+      uint8_t* p = mine + slot * stage;
+      span_load(p, dy + base * a.cols, n, st, snt);
+      span_load(p + one, h + base * a.cols, n, st, snt);
+      if (dh != nullptr) span_load(p + 2 * one, dh + base * a.cols, n, st, snt);
+    }
+    span_commit();
+  };
+  float mean[R], rstd[R];
+  auto fetch_stats = [&](int64_t base) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool live = row0 + r < a.rows;
-      mean[r] = live ? __ldg(a.mean + row0 + r) : 0.f;
-      rstd[r] = live ? __ldg(a.rstd + row0 + r) : 0.f;
+      const int64_t row = base + r * kGroups + grp;
+      mean[r] = row < a.rows ? __ldg(a.mean + row) : 0.f;
+      rstd[r] = row < a.rows ? __ldg(a.rstd + row) : 0.f;
+    }
+  };
+  int64_t ahead = unit * kRows;
+  fetch_stats(ahead);
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i, ahead += units * kRows) fetch(ahead, i);
+  int par = 0, slot = 0;
+  // every thread of a warp (block) makes the same number of steps: the sums synchronise
+  for (int64_t base = unit * kRows; base < a.rows; base += units * kRows, ahead += units * kRows, par ^= 1) {
+    fetch(ahead, slot == 0 ? STAGES - 1 : slot - 1);
+    span_wait<STAGES - 1>();
+    span_sync<kBlock>();
+    const int live = rows_at(base);
+    uint8_t* p = mine + slot * stage;
+    const T *ey = span_elems(p, dy + base * a.cols), *ez = span_elems(p + one, h + base * a.cols);
+    uint64_t g[R][CH][4], z[R][CH][4];
+    float rs[R], c1[R], c2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t nm = both(-mean[r]), rs2 = both(rstd[r]);
+      uint64_t s1[2] = {0, 0}, s2[2] = {0, 0};
+      rs[r] = rstd[r];
+      const int q = r * kGroups + grp;
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        const int32_t ch = lane + k * step;
-        cy[r][k].clear();
-        cz[r][k].clear();
-        if (live && ch < n8) {
-          const int64_t at = (row0 + r) * a.cols + ch * 8;
-          const int n = VEC ? 8 : min(8, a.cols - ch * 8);
-          if (VEC) cy[r][k].load(dy + at); else cy[r][k].load_n(dy + at, n);
-          if (VEC) cz[r][k].load(h + at); else cz[r][k].load_n(h + at, n);
+        const int c0 = (lane + k * step) * 8, e0 = q * a.cols + c0, n = q < live ? a.cols - c0 : 0;
+        span_get<T, VEC>(ey, e0, n, g[r][k]);
+        span_get<T, VEC>(ez, e0, n, z[r][k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t y = g[r][k][i];
+          z[r][k][i] = mul_f32x2(add_f32x2(z[r][k][i], nm), rs2);
+          dw[k][i] = fma_f32x2(y, z[r][k][i], dw[k][i]);
+          db[k][i] = add_f32x2(db[k][i], y);
+          g[r][k][i] = mul_f32x2(y, w[k][i]);
+          s1[i & 1] = add_f32x2(s1[i & 1], g[r][k][i]);
+          s2[i & 1] = fma_f32x2(g[r][k][i], z[r][k][i], s2[i & 1]);
         }
       }
+      c1[r] = sum_f32x2(add_f32x2(s1[0], s1[1]));
+      c2[r] = sum_f32x2(add_f32x2(s2[0], s2[1]));
     }
-    float c1[R], c2[R];
+    fetch_stats(base + units * kRows);
+#pragma unroll
+    for (int r = 0; r < R; ++r) row_sum2<TPR>(c1[r], c2[r], red[par][r]);
+    const T* ed = span_elems(p + 2 * one, dh + base * a.cols);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      c1[r] = 0.f;
-      c2[r] = 0.f;
+      const uint64_t n1 = both(-c1[r] * inv_n), n2 = both(-c2[r] * inv_n), rs2 = both(rs[r]);
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        float y8[8], z8[8];
-        cy[r][k].get(y8);
-        cz[r][k].get(z8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float z = (z8[i] - mean[r]) * rstd[r], g = y8[i] * w[k][i];
-          dw[k][i] = fmaf(y8[i], z, dw[k][i]);
-          db[k][i] += y8[i];
-          c1[r] += g;
-          c2[r] = fmaf(g, z, c2[r]);
-        }
-      }
-      row_sum2<TPR>(c1[r], c2[r], red[par][r]);
-      c1[r] *= inv_n;
-      c2[r] *= inv_n;
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (row0 + r >= a.rows) continue;
-#pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const int32_t ch = lane + k * step;
-        if (ch >= n8) continue;
-        const int64_t at = (row0 + r) * a.cols + ch * 8;
-        const int n = VEC ? 8 : min(8, a.cols - ch * 8);
-        float y8[8], z8[8], o[8];
-        cy[r][k].get(y8);
-        cz[r][k].get(z8);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float z = (z8[i] - mean[r]) * rstd[r];
-          o[i] = (fmaf(y8[i], w[k][i], -c1[r]) - z * c2[r]) * rstd[r];
-        }
-        Chunk<T> c;
+        for (int i = 0; i < 4; ++i)
+          g[r][k][i] = mul_f32x2(fma_f32x2(z[r][k][i], n2, add_f32x2(g[r][k][i], n1)), rs2);
         if (dh != nullptr) {
-          if (VEC) c.load(dh + at); else c.load_n(dh + at, n);
-          float g[8];
-          c.get(g);
+          const int q = r * kGroups + grp, c0 = (lane + k * step) * 8;
+          uint64_t d2[4];
+          span_get<T, VEC>(ed, q * a.cols + c0, q < live ? a.cols - c0 : 0, d2);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] += g[i];
-        }
-        if (dres != nullptr) {
-          c.put(o);
-          if (VEC) c.store(dres + at); else c.store_n(dres + at, n);
-        }
-        if (dx != nullptr) {
-          if (a.drop.thr > 0) {
-            const uint32_t keep = philox_keep(philox_block(static_cast<uint64_t>(row0 + r) * n8 + ch, key), a.drop.thr);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = (keep >> i) & 1u ? o[i] * a.drop.scale : 0.f;
-          }
-          c.put(o);
-          if (VEC) c.store(dx + at); else c.store_n(dx + at, n);
+          for (int i = 0; i < 4; ++i) g[r][k][i] = add_f32x2(g[r][k][i], d2[i]);
         }
       }
     }
+    // dresidual as it is, dx through the mask
+#pragma unroll
+    for (int out = 0; out < 2; ++out) {
+      T* dst = static_cast<T*>(out == 0 ? a.dres : a.dx);
+      if (dst == nullptr) continue;
+      if (!VEC) span_sync<kBlock>();   // the slot's values are in registers (or stored): it carries the output
+      T* eo = span_elems(p, dst + base * a.cols);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int q = r * kGroups + grp;
+        if (q >= live) continue;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+          const int32_t ch = lane + k * step;
+          if (ch >= n8) continue;
+          uint64_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = g[r][k][i];
+          if (out == 1 && a.drop.thr > 0) drop_pairs(v, static_cast<uint64_t>(base + q) * n8 + ch, key, a.drop);
+          if constexpr (VEC) {
+            Chunk<T> o;
+            o.put2(v);
+            o.store(dst + (base + q) * a.cols + ch * 8);
+          } else {
+            const int n = min(8, a.cols - ch * 8);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float u, t;
+              f32x2_split(v[i], u, t);
+              if (2 * i < n) eo[q * a.cols + ch * 8 + 2 * i] = from_f<T>(u);
+              if (2 * i + 1 < n) eo[q * a.cols + ch * 8 + 2 * i + 1] = from_f<T>(t);
+            }
+          }
+        }
+      }
+      if (!VEC) {
+        span_sync<kBlock>();
+        span_store(p, dst + base * a.cols, live * a.cols, st, snt);
+      }
+    }
+    span_sync<kBlock>();   // every thread is done with the slot: the next step's fetch fills it
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
   }
+  span_wait<0>();
   if (a.partial == nullptr) return;
   float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
   float* pb = pw + static_cast<int64_t>(gridDim.x) * a.cols;
@@ -175,11 +221,15 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
 #pragma unroll
       for (int k = 0; k < CH; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float s = pass ? db[k][i] : dw[k][i];
+        for (int i = 0; i < 4; ++i) {
+          float u[2];
+          f32x2_split(pass ? db[k][i] : dw[k][i], u[0], u[1]);
 #pragma unroll
-          for (int o = 16; o >= TPR; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if ((static_cast<int>(threadIdx.x) & 31) < TPR) acc[warp][(lane + k * TPR) * 8 + i] = s;
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int o = 16; o >= TPR; o >>= 1) u[j] += __shfl_xor_sync(0xffffffffu, u[j], o);
+            if ((static_cast<int>(threadIdx.x) & 31) < TPR) acc[warp][(lane + k * TPR) * 8 + 2 * i + j] = u[j];
+          }
         }
       __syncthreads();
       for (int32_t c = static_cast<int32_t>(threadIdx.x); c < a.cols; c += 256) {
@@ -194,11 +244,214 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
     for (int k = 0; k < CH; ++k) {
       const int32_t c0 = (lane + k * step) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c0 + i < a.cols) {
-          pw[c0 + i] = dw[k][i];
-          pb[c0 + i] = db[k][i];
+      for (int i = 0; i < 4; ++i) {
+        float u[2], v[2];
+        f32x2_split(dw[k][i], u[0], u[1]);
+        f32x2_split(db[k][i], v[0], v[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (c0 + 2 * i + j < a.cols) {
+            pw[c0 + 2 * i + j] = u[j];
+            pb[c0 + 2 * i + j] = v[j];
+          }
+      }
+    }
+  }
+}
+
+// The same for rows of a multiple of eight columns (see Own).
+// DROP: with dropout, whose generator takes registers that the other calls use for more warps.
+template <typename T, bool DROP, int TPR, int CH, int R, int STAGES>
+__global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 ? 2 : 1) norm_bwd_vec_kernel(const NormBwdArgs a) {
+  constexpr bool kBlock = TPR == 0;
+  constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
+  constexpr int kRows = kGroups * R;   // rows of a warp's (block's) step
+  constexpr int kParts = Own<T>::kParts;
+  constexpr int kChunkBytes = 16 * kParts;
+  __shared__ float2 red[2][R][32];
+  extern __shared__ __align__(16) uint8_t bufs[];
+  const int lane = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x & 31) % (TPR > 0 ? TPR : 1);
+  const int grp = kBlock ? 0 : static_cast<int>(threadIdx.x & 31) / (TPR > 0 ? TPR : 1);
+  const int step = kBlock ? static_cast<int>(blockDim.x) : TPR;
+  const uint32_t part = 16u * (kBlock ? blockDim.x : 256u);
+  const int64_t unit = kBlock ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t units = kBlock ? gridDim.x : static_cast<int64_t>(gridDim.x) * 8;
+  const int32_t n8 = a.cols >> 3;
+  const bool has_dh = a.dh != nullptr;
+  const uint32_t arr = static_cast<uint32_t>(R * CH * kParts) * part;   // one array of one stage
+  const uint32_t stage = (has_dh ? 3 : 2) * arr;
+  const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(bufs)) + 16 * threadIdx.x;
+  PhiloxKey key{};
+  if (DROP) key = philox_key(a.drop.rng);
+  uint64_t w[CH][4], dw[CH][4], db[CH][4];   // pairs of columns
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int32_t ch = lane + k * step;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[k][i] = both(1.f);
+      dw[k][i] = 0;
+      db[k][i] = 0;
+    }
+    if (a.weight != nullptr && ch < n8) load_param2<T, true>(a.weight, a.wfp32, ch * 8, 8, w[k]);
+  }
+  const float inv_n = 1.0f / static_cast<float>(a.cols);
+  const int64_t row_bytes = static_cast<int64_t>(a.cols) * sizeof(T);
+  const int64_t step_bytes = units * kRows * row_bytes, r_bytes = kGroups * row_bytes;
+  const int k_bytes = step * kChunkBytes;
+  const int64_t row0 = unit * kRows + grp, off0 = row0 * row_bytes + lane * kChunkBytes;   // see the forward
+  const int64_t step_rows = units * kRows;
+  const char *py = static_cast<const char*>(a.dy) + off0, *pz = static_cast<const char*>(a.h) + off0,
+             *pd = static_cast<const char*>(a.dh) + off0;
+  int64_t left_in = a.rows - row0;
+  auto fetch = [&](uint32_t at) {
+    const int left = static_cast<int>(left_in < 4096 ? left_in : 4096);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        // what does not exist reads as zero and adds nothing to any sum
+        const bool ok = r * kGroups < left && lane + k * step < n8;
+        const int64_t o = ok ? r * r_bytes + k * k_bytes : 0;
+        const uint32_t d = at + static_cast<uint32_t>((r * CH + k) * kParts) * part;
+        Own<T>::copy_or_zero(d, part, (ok ? py : static_cast<const char*>(a.dy)) + o, ok);
+        Own<T>::copy_or_zero(d + arr, part, (ok ? pz : static_cast<const char*>(a.h)) + o, ok);
+        if (has_dh) Own<T>::copy_or_zero(d + 2 * arr, part, (ok ? pd : static_cast<const char*>(a.dh)) + o, ok);
+      }
+    span_commit();
+    left_in -= step_rows;
+    py += step_bytes;
+    pz += step_bytes;
+    pd += step_bytes;
+  };
+  int64_t row = row0, left64 = left_in;
+  char *po = static_cast<char*>(a.dres) + off0, *px = static_cast<char*>(a.dx) + off0;
+  float mean[R], rstd[R];
+  auto fetch_stats = [&](int64_t first) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t q = first + r * kGroups;
+      mean[r] = q < a.rows ? __ldg(a.mean + q) : 0.f;
+      rstd[r] = q < a.rows ? __ldg(a.rstd + q) : 0.f;
+    }
+  };
+  fetch_stats(row);
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(sm + i * stage);
+  uint32_t cur = 0;
+  int par = 0;
+  // every thread of a warp (block) makes the same number of steps: the sums synchronise
+  for (int64_t base = unit * kRows; base < a.rows; base += step_rows, par ^= 1) {
+    const int left = static_cast<int>(left64 < 4096 ? left64 : 4096);
+    fetch(sm + (cur == 0 ? (STAGES - 1) * stage : cur - stage));
+    span_wait<STAGES - 1>();
+    uint64_t g[R][CH][4], z[R][CH][4];
+    float rs[R], c1[R], c2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t nm = both(-mean[r]), rs2 = both(rstd[r]);
+      uint64_t s1[2] = {0, 0}, s2[2] = {0, 0};
+      rs[r] = rstd[r];
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const uint32_t d = sm + cur + static_cast<uint32_t>((r * CH + k) * kParts) * part;
+        Own<T>::read(d, part, g[r][k]);
+        Own<T>::read(d + arr, part, z[r][k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t y = g[r][k][i];
+          z[r][k][i] = mul_f32x2(add_f32x2(z[r][k][i], nm), rs2);
+          dw[k][i] = fma_f32x2(y, z[r][k][i], dw[k][i]);
+          db[k][i] = add_f32x2(db[k][i], y);
+          g[r][k][i] = mul_f32x2(y, w[k][i]);
+          s1[i & 1] = add_f32x2(s1[i & 1], g[r][k][i]);
+          s2[i & 1] = fma_f32x2(g[r][k][i], z[r][k][i], s2[i & 1]);
         }
+      }
+      c1[r] = sum_f32x2(add_f32x2(s1[0], s1[1]));
+      c2[r] = sum_f32x2(add_f32x2(s2[0], s2[1]));
+    }
+    fetch_stats(row + step_rows);
+#pragma unroll
+    for (int r = 0; r < R; ++r) row_sum2<TPR>(c1[r], c2[r], red[par][r]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint64_t n1 = both(-c1[r] * inv_n), n2 = both(-c2[r] * inv_n), rs2 = both(rs[r]);
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          g[r][k][i] = mul_f32x2(fma_f32x2(z[r][k][i], n2, add_f32x2(g[r][k][i], n1)), rs2);
+        if (has_dh) {
+          uint64_t d2[4];
+          Own<T>::read(sm + cur + 2 * arr + static_cast<uint32_t>((r * CH + k) * kParts) * part, part, d2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) g[r][k][i] = add_f32x2(g[r][k][i], d2[i]);
+        }
+        if (r * kGroups < left && lane + k * step < n8) {
+          if (a.dres != nullptr) Own<T>::write(po + r * r_bytes + k * k_bytes, g[r][k]);
+          if (a.dx != nullptr) {
+            if (DROP)
+              drop_pairs(g[r][k], static_cast<uint64_t>(row + r * kGroups) * n8 + (lane + k * step), key, a.drop);
+            Own<T>::write(px + r * r_bytes + k * k_bytes, g[r][k]);
+          }
+        }
+      }
+    }
+    cur = cur + stage == STAGES * stage ? 0 : cur + stage;
+    left64 -= step_rows;
+    row += step_rows;
+    po += step_bytes;
+    px += step_bytes;
+  }
+  span_wait<0>();
+  if (a.partial == nullptr) return;
+  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
+  float* pb = pw + static_cast<int64_t>(gridDim.x) * a.cols;
+  if constexpr (TPR > 0) {
+    // the block's groups: those of a warp by shuffles, the warps through shared memory
+    __shared__ float acc[8][32 * CH * 8];
+    const int warp = static_cast<int>(threadIdx.x) >> 5;
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass) __syncthreads();
+#pragma unroll
+      for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float u[2];
+          f32x2_split(pass ? db[k][i] : dw[k][i], u[0], u[1]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int o = 16; o >= TPR; o >>= 1) u[j] += __shfl_xor_sync(0xffffffffu, u[j], o);
+            if ((static_cast<int>(threadIdx.x) & 31) < TPR) acc[warp][(lane + k * TPR) * 8 + 2 * i + j] = u[j];
+          }
+        }
+      __syncthreads();
+      for (int32_t c = static_cast<int32_t>(threadIdx.x); c < a.cols; c += 256) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += acc[q][c];
+        (pass ? pb : pw)[c] = s;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int32_t c0 = (lane + k * step) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float u[2], v[2];
+        f32x2_split(dw[k][i], u[0], u[1]);
+        f32x2_split(db[k][i], v[0], v[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (c0 + 2 * i + j < a.cols) {
+            pw[c0 + 2 * i + j] = u[j];
+            pb[c0 + 2 * i + j] = v[j];
+          }
+      }
     }
   }
 }
@@ -232,55 +485,68 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
   }
 }
 
-// Launch shape of the first kernel: threads of a block, rows of a block's step, blocks.
+// Launch shape of the first kernel: threads that share a row (0: the block), threads of a
+// block, blocks.  It depends on the sizes alone, and so do the parts and the sums' order.
 struct BwdShape {
-  int tpr, ch, r;       // template arguments
-  int threads;
+  int tpr, threads;
   int64_t blocks;
 };
 
 BwdShape bwd_shape(int64_t rows, int32_t cols) {
   const int n8 = (cols + 7) >> 3;
   BwdShape s{};
-  if (n8 <= 1) { s.tpr = 1; s.ch = 1; s.r = 2; }
-  else if (n8 <= 4) { s.tpr = 4; s.ch = 1; s.r = 2; }
-  else if (n8 <= 16) { s.tpr = 16; s.ch = 1; s.r = 2; }
-  else if (n8 <= 32) { s.tpr = 32; s.ch = 1; s.r = 2; }
-  else if (n8 <= 64) { s.tpr = 32; s.ch = 2; s.r = 1; }
-  else if (n8 <= 512) { s.tpr = 0; s.ch = 1; s.r = 2; }
-  else if (n8 <= 1024) { s.tpr = 0; s.ch = 2; s.r = 1; }
-  else { s.tpr = 0; s.ch = 4; s.r = 1; }
+  s.tpr = n8 <= 1 ? 1 : n8 <= 4 ? 2 : n8 <= 8 ? 4 : n8 <= 16 ? 8 : n8 <= 32 ? 16 : n8 <= 64 ? 32 : 0;
   int per_sm;
   int64_t block_rows;
   if (s.tpr > 0) {
     s.threads = 256;
-    block_rows = static_cast<int64_t>(256 / s.tpr) * s.r;
-    per_sm = 3;
+    block_rows = static_cast<int64_t>(256 / s.tpr);
+    per_sm = 2;
   } else {
-    s.threads = ((n8 + s.ch - 1) / s.ch + 31) / 32 * 32;
-    block_rows = s.r;
-    per_sm = 768 / s.threads;
-    per_sm = per_sm < 1 ? 1 : (per_sm > 8 ? 8 : per_sm);
+    const int ch = n8 <= 512 ? 1 : 2;
+    s.threads = ((n8 + ch - 1) / ch + 31) / 32 * 32;
+    block_rows = ch == 1 ? 2 : 1;
+    per_sm = (ch == 1 ? 1024 : 640) / s.threads;
+    per_sm = per_sm < 1 ? 1 : per_sm;
   }
   const int64_t need = (rows + block_rows - 1) / block_rows;
   s.blocks = need < 148 * per_sm ? need : 148 * per_sm;
   return s;
 }
 
+template <typename T, bool VEC, int TPR, int CH, int R, int STAGES>
+cudaError_t launch_bwd(const NormBwdArgs& a, const BwdShape& s, cudaStream_t stream) {
+  void (*kern)(NormBwdArgs);
+  if constexpr (VEC)
+    kern = a.drop.thr > 0 ? norm_bwd_vec_kernel<T, true, TPR, CH, R, STAGES> : norm_bwd_vec_kernel<T, false, TPR, CH, R, STAGES>;
+  else
+    kern = norm_bwd_kernel<T, TPR, CH, R, STAGES>;
+  constexpr int rows = (TPR > 0 ? 32 / (TPR > 0 ? TPR : 1) : 1) * R;
+  const int units = TPR > 0 ? s.threads / 32 : 1;
+  const int stage = VEC ? R * CH * s.threads * 8 * static_cast<int>(sizeof(T))
+                        : units * static_cast<int>(span_bytes<T>(static_cast<uint32_t>(rows) * a.cols));
+  const int smem = STAGES * (a.dh != nullptr ? 3 : 2) * stage;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(s.blocks), s.threads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, bool VEC>
 cudaError_t bwd_t(const NormBwdArgs& a, cudaStream_t stream) {
   const BwdShape s = bwd_shape(a.rows, a.cols);
-  const unsigned g = static_cast<unsigned>(s.blocks);
   if (a.rows > 0) {
-    if (s.tpr == 1) norm_bwd_kernel<T, VEC, 1, 1, 2><<<g, s.threads, 0, stream>>>(a);
-    else if (s.tpr == 4) norm_bwd_kernel<T, VEC, 4, 1, 2><<<g, s.threads, 0, stream>>>(a);
-    else if (s.tpr == 16) norm_bwd_kernel<T, VEC, 16, 1, 2><<<g, s.threads, 0, stream>>>(a);
-    else if (s.tpr == 32 && s.ch == 1) norm_bwd_kernel<T, VEC, 32, 1, 2><<<g, s.threads, 0, stream>>>(a);
-    else if (s.tpr == 32) norm_bwd_kernel<T, VEC, 32, 2, 1><<<g, s.threads, 0, stream>>>(a);
-    else if (s.ch == 1) norm_bwd_kernel<T, VEC, 0, 1, 2><<<g, s.threads, 0, stream>>>(a);
-    else if (s.ch == 2) norm_bwd_kernel<T, VEC, 0, 2, 1><<<g, s.threads, 0, stream>>>(a);
-    else norm_bwd_kernel<T, VEC, 0, 4, 1><<<g, s.threads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    switch (s.tpr) {
+      case 1: e = launch_bwd<T, VEC, 1, 1, 1, 4>(a, s, stream); break;
+      case 2: e = launch_bwd<T, VEC, 2, 2, 1, 4>(a, s, stream); break;
+      case 4: e = launch_bwd<T, VEC, 4, 2, 1, 4>(a, s, stream); break;
+      case 8: e = launch_bwd<T, VEC, 8, 2, 1, 4>(a, s, stream); break;
+      case 16: e = launch_bwd<T, VEC, 16, 2, 1, 4>(a, s, stream); break;
+      case 32: e = launch_bwd<T, VEC, 32, 2, 1, 4>(a, s, stream); break;
+      default:
+        e = a.cols <= 4096 ? launch_bwd<T, VEC, 0, 1, 2, 2>(a, s, stream) : launch_bwd<T, VEC, 0, 2, 1, 2>(a, s, stream);
+    }
     if (e != cudaSuccess) return e;
   }
   if (a.dweight != nullptr || a.dbias != nullptr) {

@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -12,9 +13,27 @@
 
 #include "norm.h"
 #include "philox.cuh"
+#include "ptx.cuh"
 
 namespace sta {
 namespace norm {
+
+using ptx::add_f32x2;
+using ptx::f32x2;
+using ptx::f32x2_split;
+using ptx::fma_f32x2;
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float v) { return f32x2(v, v); }
+__device__ __forceinline__ float sum_f32x2(uint64_t v) {
+  float a, b;
+  f32x2_split(v, a, b);
+  return a + b;
+}
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
@@ -72,17 +91,52 @@ struct Chunk {
   }
   __device__ __forceinline__ void get_t(T (&e)[8]) const;
   __device__ __forceinline__ void set(const T (&e)[8]);
+  // to fp32, and from fp32 with one rounding (two at a time: the packed conversions run at
+  // several times the rate of single ones, which bounded these kernels otherwise)
   __device__ __forceinline__ void get(float (&f)[8]) const {
-    T e[8];
-    get_t(e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = to_f<T>(e[i]);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        f[2 * i] = __uint_as_float(w[2 * i]);
+        f[2 * i + 1] = __uint_as_float(w[2 * i + 1]);
+      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    }
+  }
+  // pairs of columns: the arithmetic runs on packed fp32 (half the instructions, which
+  // bound these kernels where memory does not)
+  __device__ __forceinline__ void get2(uint64_t (&f)[4]) const {
+    float v[8];
+    get(v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f32x2(v[2 * i], v[2 * i + 1]);
+  }
+  __device__ __forceinline__ void put2(const uint64_t (&f)[4]) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f32x2_split(f[i], v[2 * i], v[2 * i + 1]);
+    put(v);
   }
   __device__ __forceinline__ void put(const float (&f)[8]) {
-    T e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = from_f<T>(f[i]);
-    set(e);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[2 * i] = __float_as_uint(f[2 * i]);
+        w[2 * i + 1] = __float_as_uint(f[2 * i + 1]);
+      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
   }
 };
 
@@ -119,6 +173,127 @@ __device__ __forceinline__ void Chunk<T>::set(const T (&e)[8]) {
   }
 }
 
+// Consecutive rows are one span of memory.  A span is copied to shared memory ahead of its
+// use, in 16-byte asynchronous copies that need no registers, and (rows whose length is no
+// multiple of eight start anywhere) back from there: in aligned blocks, at the same offset
+// inside a block on both sides, element by element only in a block that the span does not
+// fill.  Element i of a span whose global address is g lies at buf + (g mod 16) + i size.
+template <typename T>
+__host__ __device__ constexpr uint32_t span_bytes(uint32_t n) {
+  return (n * static_cast<uint32_t>(sizeof(T)) + 15) / 16 * 16 + 16;
+}
+template <typename T>
+__device__ __forceinline__ T* span_elems(uint8_t* buf, const T* g) {
+  return reinterpret_cast<T*>(buf + (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(g)) & 15u));
+}
+// Starts the copy of n elements from g, by threads t, t + nt, ... (commit and wait by the caller).
+template <typename T>
+__device__ __forceinline__ void span_load(uint8_t* buf, const T* g, int n, int t, int nt) {
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(g)) & 15u;
+  const uint32_t end = off + static_cast<uint32_t>(n) * sizeof(T);
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(g) - off;
+  const uint32_t sbuf = static_cast<uint32_t>(__cvta_generic_to_shared(buf));
+  for (uint32_t b = static_cast<uint32_t>(t) * 16; b < end; b += static_cast<uint32_t>(nt) * 16) {
+    if (b >= off && b + 16 <= end) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sbuf + b), "l"(base + b) : "memory");
+    } else {
+      const uint32_t lo = b < off ? off : b, hi = b + 16 < end ? b + 16 : end;
+      for (uint32_t x = lo; x < hi; x += sizeof(T)) *reinterpret_cast<T*>(buf + x) = *reinterpret_cast<const T*>(base + x);
+    }
+  }
+}
+__device__ __forceinline__ void span_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void span_wait() {   // all but this thread's last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void span_store(const uint8_t* buf, T* g, int n, int t, int nt) {
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(g)) & 15u;
+  const uint32_t end = off + static_cast<uint32_t>(n) * sizeof(T);
+  uint8_t* base = reinterpret_cast<uint8_t*>(g) - off;
+  for (uint32_t b = static_cast<uint32_t>(t) * 16; b < end; b += static_cast<uint32_t>(nt) * 16) {
+    if (b >= off && b + 16 <= end) {
+      *reinterpret_cast<uint4*>(base + b) = *reinterpret_cast<const uint4*>(buf + b);
+    } else {
+      const uint32_t lo = b < off ? off : b, hi = b + 16 < end ? b + 16 : end;
+      for (uint32_t x = lo; x < hi; x += sizeof(T)) *reinterpret_cast<T*>(base + x) = *reinterpret_cast<const T*>(buf + x);
+    }
+  }
+}
+// Eight elements of a span from e0 on, as pairs of fp32; those from n on read as zero.
+template <typename T, bool VEC>
+__device__ __forceinline__ void span_get(const T* e, int e0, int n, uint64_t (&f)[4]) {
+  if constexpr (VEC) {
+    Chunk<T> c;
+    const uint4* q = reinterpret_cast<const uint4*>(e + e0);
+#pragma unroll
+    for (int i = 0; i < Chunk<T>::kWords / 4; ++i) {
+      const uint4 v = n > 0 ? q[i] : make_uint4(0u, 0u, 0u, 0u);
+      c.w[4 * i] = v.x; c.w[4 * i + 1] = v.y; c.w[4 * i + 2] = v.z; c.w[4 * i + 3] = v.w;
+    }
+    c.get2(f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = f32x2(2 * i < n ? to_f<T>(e[e0 + 2 * i]) : 0.f, 2 * i + 1 < n ? to_f<T>(e[e0 + 2 * i + 1]) : 0.f);
+  }
+}
+// Pairs through the dropout mask.  Dropped values are replaced, not multiplied by zero: an
+// infinity or NaN there stays out.
+__device__ __forceinline__ void drop_pairs(uint64_t (&f)[4], uint64_t block, const PhiloxKey& key, const NormDropout& d) {
+  const uint32_t keep = philox_keep(philox_block(block, key), d.thr);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float u, v;
+    f32x2_split(f[i], u, v);
+    f[i] = f32x2((keep >> (2 * i)) & 1u ? u * d.scale : 0.f, (keep >> (2 * i + 1)) & 1u ? v * d.scale : 0.f);
+  }
+}
+
+// Rows of a multiple of eight columns: every chunk is aligned, and a thread copies the
+// chunks it will use itself, ahead of their use, into places of its own in shared memory
+// (16 bytes of each thread side by side).  No other thread reads them, so waiting for its
+// own copies is all a thread needs.
+// 16 bytes where `ok`; otherwise zeros (src is then any valid address and is not read).
+__device__ __forceinline__ void own_copy_or_zero(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ uint4 own_read(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
+// A chunk is kParts 16-byte parts; part p of chunk i of a stage lies at (i kParts + p) 16 threads + 16 thread.
+template <typename T>
+struct Own {
+  static constexpr int kParts = static_cast<int>(sizeof(T)) / 2;
+  static __device__ __forceinline__ void copy_or_zero(uint32_t at, uint32_t part, const char* src, bool ok) {
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) own_copy_or_zero(at + p * part, src + 16 * p, ok);
+  }
+  static __device__ __forceinline__ void read(uint32_t at, uint32_t part, uint64_t (&f)[4]) {
+    Chunk<T> c;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const uint4 v = own_read(at + p * part);
+      c.w[4 * p] = v.x; c.w[4 * p + 1] = v.y; c.w[4 * p + 2] = v.z; c.w[4 * p + 3] = v.w;
+    }
+    c.get2(f);
+  }
+  static __device__ __forceinline__ void write(char* dst, const uint64_t (&f)[4]) {
+    Chunk<T> c;
+    c.put2(f);
+    c.store(reinterpret_cast<T*>(dst));
+  }
+};
+
+// Barrier of the threads that share a span: a warp, or the block.
+template <bool BLOCK>
+__device__ __forceinline__ void span_sync() {
+  if (BLOCK) __syncthreads(); else __syncwarp();
+}
+
 // Columns c .. c + 7 of the weight or bias as fp32 (n of them exist; the rest read as zero).
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_param(const void* p, bool fp32, int32_t c, int n, float (&f)[8]) {
@@ -145,8 +320,37 @@ __device__ __forceinline__ void load_param(const void* p, bool fp32, int32_t c, 
   }
 }
 
+// The eight parameters at p, an address in an array of `fp32` or T elements.
+template <typename T>
+__device__ __forceinline__ void read_param2(const char* p, bool fp32, uint64_t (&f)[4]) {
+  if (fp32) {
+    const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p)), b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = b.x;
+    f[3] = b.y;
+  } else {
+    Chunk<T> k;
+#pragma unroll
+    for (int i = 0; i < Chunk<T>::kWords / 4; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      k.w[4 * i] = v.x; k.w[4 * i + 1] = v.y; k.w[4 * i + 2] = v.z; k.w[4 * i + 3] = v.w;
+    }
+    k.get2(f);
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_param2(const void* p, bool fp32, int32_t c, int n, uint64_t (&f)[4]) {
+  float v[8];
+  load_param<T, VEC>(p, fp32, c, n, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f32x2(v[2 * i], v[2 * i + 1]);
+}
+
 // Sum over the TPR threads that share a row (TPR = 0: the whole block, through `red`,
-// which holds 32 floats; every thread of the block calls it).
+// which holds 32 floats; every thread of the block calls it).  One barrier: successive
+// calls take two buffers in turn, so that a buffer is written again only after the other
+// call's barrier.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* red) {
   if constexpr (TPR > 0) {
@@ -154,13 +358,14 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     for (int o = TPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   } else {
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     const int warps = static_cast<int>(blockDim.x) >> 5;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     float s = static_cast<int>(threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f;
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    __syncthreads();
     return s;
   }
 }
