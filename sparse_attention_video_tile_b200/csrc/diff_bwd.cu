@@ -5,14 +5,14 @@
 //   dQ_m = scale dS_m K_m,  dK_m = scale dS_m^T Q_m,  dV = (P_1 - lambda P_2)^T dO,
 //   dlambda = - sum over rows of sum_j P_2 dP.
 //
-// Four launches:
+// Three launches:
 //   * prep (HBM bound): q, k, v, dO copied into the tiled order of the padded latent,
 //     and per row -lse_m in log2 units and -D_m, with D_2 = dO . O_2 and
 //     D_1 = dO . out + lambda D_2 from the stored outputs.  Pad rows get P = 0
 //     (-lse = -inf) and D = 0, so that they add nothing anywhere;
 //   * dQ over query blocks and the key blocks of their windows;
-//   * dK, dV over key blocks and the query blocks that attend them;
-//   * the sum of dlambda's parts.
+//   * dK, dV over key blocks and the query blocks that attend them; its first blocks also
+//     add dlambda's parts, which the dQ kernel left per item.
 // Per 128 x 128 block the tensor cores do 1536 clocks of work in the dQ kernel (S_1,
 // S_2, dP, dQ_1, dQ_2) and 2048 in the other (S_1, S_2, dP, dV, dK_1, dK_2), at 64 per
 // M128 N128 K16, and both rebuild 2 x 128 x 128 exponentials (2048 clocks of MUFU).
@@ -42,7 +42,8 @@ struct BwdParams {
   const float* lam;
   const float* vec;        // [4][BH][Lpad]: -lse_1, -lse_2 (log2 units), -D_1, -D_2
   __nv_bfloat16 *o0, *o1;  // dq; or dk and dv
-  float* part;             // dQ kernel: [item][4] sums of P_2 dP
+  float* part;             // [item][4] sums of P_2 dP: the dQ kernel writes them, the dK, dV kernel adds them
+  float* dlam;
   int32_t n_items;
   float scale, scale_log2;
   int32_t* err;
@@ -132,21 +133,23 @@ __global__ void __launch_bounds__(256) diff_prep_kernel(const uint4* __restrict_
   }
 }
 
-// dlambda[head] = - sum of the dQ items' parts, in a fixed order.
-__global__ void __launch_bounds__(256) diff_dlam_kernel(const float* __restrict__ part, float* __restrict__ dlam,
-                                                        const __grid_constant__ DiffGeo g) {
-  __shared__ float red[8];
-  const int64_t n = static_cast<int64_t>(g.batch) * g.blocks * 4;   // the head's items lie together
-  const float* p = part + n * blockIdx.x;
-  float s = 0.f;
-  for (int64_t i = threadIdx.x; i < n; i += 256) s += p[i];
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0.f;
-    for (int i = 0; i < 8; ++i) s += red[i];
-    dlam[g.order[blockIdx.x]] = -s;
+// dlambda[head] = - sum of the dQ items' parts, in a fixed order, by all threads of a block
+// (`red`: kThreads / 32 floats of shared memory).
+__device__ __forceinline__ void sum_dlambda(const DiffGeo& g, const float* part, float* dlam, float* red) {
+  const int64_t n = static_cast<int64_t>(g.batch) * g.blocks * 4;   // a head's items lie together
+  for (int32_t i = static_cast<int32_t>(blockIdx.x); i < g.heads; i += static_cast<int32_t>(gridDim.x)) {
+    const float* p = part + n * i;
+    float s = 0.f;
+    for (int64_t x = threadIdx.x; x < n; x += kThreads) s += p[x];
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s = 0.f;
+      for (int x = 0; x < kThreads / 32; ++x) s += red[x];
+      dlam[g.order[i]] = -s;
+    }
+    __syncthreads();
   }
 }
 
@@ -176,7 +179,8 @@ struct Dq {
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
 
-template <int D>
+// PAD: some tile has pad tokens; the elementwise warps then walk the blocks and mask their keys.
+template <int D, bool PAD>
 __global__ void __launch_bounds__(kThreads, 1)
     diff_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -220,7 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<uint32_t*>(smem + S::kSlot);
   const WaitCtx wc{abort_flag, p.err, p.limit_ns};
   const DiffGeo& g = p.g;
-  const int32_t stride = static_cast<int32_t>(gridDim.x), first = static_cast<int32_t>(blockIdx.x);
 
   if (warp >= 8) {
     setmaxnreg_dec<kRegsOther>();
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- Q, dO and K loads
       uint32_t seq = 0, k = 0;
       bool ok = true;
-      for (int32_t idx = first; ok && idx < p.n_items; idx += stride) {
+      for (int32_t turn = 0, idx = item_at(0); ok && idx < p.n_items; idx = item_at(++turn)) {
         const Item it = get_item<false>(g, idx);
         ok = mbar_wait(sb + S::kFixEmpty, (k & 1) ^ 1, wc, 0x31);
         if (!ok) break;
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- V loads
       uint32_t seq = 0;
       bool ok = true;
-      for (int32_t idx = first; ok && idx < p.n_items; idx += stride) {
+      for (int32_t turn = 0, idx = item_at(0); ok && idx < p.n_items; idx = item_at(++turn)) {
         const Item it = get_item<false>(g, idx);
         Block b = first_block(it);
         for (int32_t j = 0; j < it.n; ++j, ++seq, next_block(g, it, b)) {
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dk0 = desc_lo(sb + S::kK, kLboK), dv0 = desc_lo(sb + S::kV, kLboK);
       uint32_t seq = 0, k = 0;
       bool ok = true;
-      for (int32_t idx = first; ok && idx < p.n_items; idx += stride, ++k) {
+      for (int32_t turn = 0, idx = item_at(0); ok && idx < p.n_items; idx = item_at(++turn), ++k) {
         const Item it = get_item<false>(g, idx);
         ok = mbar_wait(sb + S::kFixFull, k & 1, wc, 0x34);
         for (int32_t j = 0; ok && j < it.n; ++j, ++seq) {
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dk0 = desc_lo(sb + S::kK, kLboMn);
       uint32_t seq = 0;
       bool ok = true;
-      for (int32_t idx = first; ok && idx < p.n_items; idx += stride) {
+      for (int32_t turn = 0, idx = item_at(0); ok && idx < p.n_items; idx = item_at(++turn)) {
         const Item it = get_item<false>(g, idx);
         for (int32_t j = 0; ok && j < it.n; ++j, ++seq) {
           const uint32_t st = seq % KS;
@@ -352,9 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t tDs = tl + 256 + 64 * m;
     const Local loc = local_of(g, row);
+    KeyPlaces places;
+    if constexpr (PAD) places.init(g);
     uint32_t seq = 0, k = 0;
     bool ok = true;
-    for (int32_t idx = first; ok && idx < p.n_items; idx += stride, ++k) {
+    for (int32_t turn = 0, idx = item_at(0); ok && idx < p.n_items; idx = item_at(++turn), ++k) {
       const Item it = get_item<false>(g, idx);
       Block b = first_block(it);
       const int32_t trow = tiled_row(g, own_block(it)) + row;
@@ -383,11 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           s[i] = __float_as_uint(ex2_approx(x0));
           s[i + 1] = __float_as_uint(ex2_approx(x1));
         }
-        if (g.padded) {
+        if constexpr (PAD) {
           if (has_pads(g, b)) {   // pad keys: exp(0 - lse) of a row with low scores could overflow
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint32_t w = real_word(g, b, c);
+              const uint32_t w = places.real(g, b, c);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!((w >> i) & 1u)) s[32 * c + i] = 0;
@@ -498,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  sum_dlambda(p.g, p.part, p.dlam, reinterpret_cast<float*>(smem));   // before any load into shared memory
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kAbort);
   if (threadIdx.x == 0) {
     mbar_init(sb + S::kFixFull, 1);
@@ -536,7 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<uint32_t*>(smem + S::kSlot);
   const WaitCtx wc{abort_flag, p.err, p.limit_ns};
   const DiffGeo& g = p.g;
-  const int32_t stride = static_cast<int32_t>(gridDim.x), first = static_cast<int32_t>(blockIdx.x);
 
   if (warp >= 8) {
     setmaxnreg_dec<kRegsOther>();
@@ -544,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- K, V of the item; Q of its blocks
       uint32_t seq = 0, k = 0;
       bool ok = true;
-      for (int32_t idx = first; ok && idx < p.n_items; idx += stride) {
+      for (int32_t turn = 0, idx = item_at(0); ok && idx < p.n_items; idx = item_at(++turn)) {
         const Item it = get_item<true>(g, idx);
         ok = mbar_wait(sb + S::kFixEmpty, (k & 1) ^ 1, wc, 0x41);
         if (!ok) break;
@@ -570,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- dO of the blocks
       uint32_t seq = 0;
       bool ok = true;
-      for (int32_t idx = first; ok && idx < p.n_items; idx += stride) {
+      for (int32_t turn = 0, idx = item_at(0); ok && idx < p.n_items; idx = item_at(++turn)) {
         const Item it = get_item<true>(g, idx);
         Block b = first_block(it);
         for (int32_t j = 0; j < it.n; ++j, ++seq, next_block(g, it, b)) {
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- -lse and -D of the blocks
       uint32_t seq = 0;
       bool ok = true, half = false;   // half: this block's lse was loaded, its D not
-      for (int32_t idx = first; ok && idx < p.n_items; idx += stride) {
+      for (int32_t turn = 0, idx = item_at(0); ok && idx < p.n_items; idx = item_at(++turn)) {
         const Item it = get_item<true>(g, idx);
         Block b = first_block(it);
         for (int32_t j = 0; j < it.n; ++j, ++seq, next_block(g, it, b)) {
@@ -648,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t i = 0;   // block of the CTA's stream
       uint32_t k = 0;
       bool ok = true;
-      for (int32_t idx = first; ok && idx < p.n_items; idx += stride, ++k) {
+      for (int32_t turn = 0, idx = item_at(0); ok && idx < p.n_items; idx = item_at(++turn), ++k) {
         const Item it = get_item<true>(g, idx);
         ok = mbar_wait(sb + S::kFixFull, k & 1, wc, 0x46) && q_full(i) && do_full(i) &&
              (i == 0 || mbar_wait(sb + S::kSFree + 8, (i - 1) & 1, wc, 0x47));
@@ -726,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kHalf = 16u << 16;   // TMEM address of lane 16
     uint32_t seq = 0, k = 0;
     bool ok = true;
-    for (int32_t idx = first; ok && idx < p.n_items; idx += stride, ++k) {
+    for (int32_t turn = 0, idx = item_at(0); ok && idx < p.n_items; idx = item_at(++turn), ++k) {
       // the loop keeps two numbers of the item: the block's P of both maps needs the registers
       int32_t n;
       uint64_t nlam2;
@@ -852,7 +857,7 @@ cudaError_t launch_t(const DiffGeo& g, const DiffBwdArgs& a, int32_t* err, uint6
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   // before the tensor maps: these calls make the device's context current in a thread that
   // has not used the device yet (autograd's), which the driver's encode call needs
-  auto dq = diff_dq_kernel<D>;
+  auto dq = g.padded ? diff_dq_kernel<D, true> : diff_dq_kernel<D, false>;
   if ((e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, Dq<D>::kBytes)) != cudaSuccess) return e;
   auto dkv = diff_dkv_kernel<D>;
   if ((e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, Dkv<D>::kBytes)) != cudaSuccess) return e;
@@ -870,6 +875,7 @@ cudaError_t launch_t(const DiffGeo& g, const DiffBwdArgs& a, int32_t* err, uint6
   p.lam = a.lam;
   p.vec = a.vec;
   p.part = a.dlam_part;
+  p.dlam = a.dlam;
   p.n_items = static_cast<int32_t>(bh * g.blocks);
   p.scale = a.scale;
   p.scale_log2 = a.scale * kLog2e;
@@ -883,8 +889,6 @@ cudaError_t launch_t(const DiffGeo& g, const DiffBwdArgs& a, int32_t* err, uint6
   p.o0 = static_cast<__nv_bfloat16*>(a.dk);
   p.o1 = static_cast<__nv_bfloat16*>(a.dv);
   dkv<<<grid, kThreads, Dkv<D>::kBytes, stream>>>(tm[0], tm[1], tm[2], tm[3], p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  diff_dlam_kernel<<<g.heads, 256, 0, stream>>>(a.dlam_part, a.dlam, g);
   return cudaGetLastError();
 }
 

@@ -143,6 +143,13 @@ __device__ __forceinline__ Item get_item(const DiffGeo& g, int32_t idx) {
   return it;
 }
 
+// Item of this CTA's turn: the grid is walked forth and back, so that the CTA with the
+// longest item of one turn has the shortest of the next (items come by decreasing window).
+__device__ __forceinline__ int32_t item_at(int32_t turn) {
+  const int32_t n = static_cast<int32_t>(gridDim.x), i = static_cast<int32_t>(blockIdx.x);
+  return turn * n + ((turn & 1) ? n - 1 - i : i);
+}
+
 // A 128-row block of the padded latent.
 struct Block {
   int32_t t, h, w, s;
@@ -158,33 +165,6 @@ __device__ __forceinline__ void next_block(const DiffGeo& g, const Item& it, Blo
   b.h = it.bh0;
   ++b.t;
 }
-// The blocks of an item's box in order, for roles that only need them to mask pads; empty otherwise.
-template <bool PAD>
-struct Walk {
-  __device__ __forceinline__ void start(const Item&) {}
-  __device__ __forceinline__ void next(const DiffGeo&) {}
-};
-template <>
-struct Walk<true> {
-  Block b;
-  int32_t h0, h1, w0, w1;
-  __device__ __forceinline__ void start(const Item& it) {
-    b = first_block(it);
-    h0 = it.bh0;
-    h1 = h0 + it.enh;
-    w0 = it.bw0;
-    w1 = w0 + it.enw;
-  }
-  __device__ __forceinline__ void next(const DiffGeo& g) {
-    if (++b.s < slabs_at(g, b.t)) return;
-    b.s = 0;
-    if (++b.w < w1) return;
-    b.w = w0;
-    if (++b.h < h1) return;
-    b.h = h0;
-    ++b.t;
-  }
-};
 // First row of a block in the tiled order of the padded latent.
 __device__ __forceinline__ int32_t tiled_row(const DiffGeo& g, const Block& b) {
   return ((b.t * g.nH + b.h) * g.nW + b.w) * g.ntile + b.s * kBlockRows;
@@ -212,10 +192,25 @@ __device__ __forceinline__ int64_t row_of(const DiffGeo& g, int32_t b, int32_t h
   return g.token_major ? (static_cast<int64_t>(b) * g.L + token) * g.heads + head
                        : (static_cast<int64_t>(b) * g.heads + head) * g.L + token;
 }
-// Bit i of word c: key 32 c + i of the block is a real token (called by a whole warp).
-__device__ __forceinline__ uint32_t real_word(const DiffGeo& g, const Block& b, int c) {
-  return __ballot_sync(0xffffffffu, token_of(g, b, local_of(g, 32 * c + static_cast<int>(threadIdx.x & 31))) >= 0);
-}
+// Which keys of a block are real tokens, 32 at a time: lane i knows the places of keys
+// 32 c + i inside a slab (8 bits each of t, h, w).
+struct KeyPlaces {
+  uint32_t at[4];
+  __device__ __forceinline__ void init(const DiffGeo& g) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const Local l = local_of(g, 32 * c + static_cast<int>(threadIdx.x & 31));
+      at[c] = static_cast<uint32_t>(l.t | (l.h << 8) | (l.w << 16));
+    }
+  }
+  // bit i: key 32 c + i of the block is real (called by a whole warp)
+  __device__ __forceinline__ uint32_t real(const DiffGeo& g, const Block& b, int c) const {
+    const uint32_t p = at[c];
+    return __ballot_sync(0xffffffffu, b.t * g.tt + b.s * g.bt + static_cast<int>(p & 255u) < g.T &&
+                                          b.h * g.th + static_cast<int>((p >> 8) & 255u) < g.H &&
+                                          b.w * g.tw + static_cast<int>(p >> 16) < g.W);
+  }
+};
 
 // Loads a block of D columns as 64-column boxes: 3-D boxes of a tiled copy, or 5-D boxes
 // (one slab) of the raster tensor, whose coordinates past the grid read as zeros.
