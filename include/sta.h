@@ -333,26 +333,16 @@ sta_status sta_attention_fwd_noalloc(const void* q, const void* k, const void* v
  *     backward needs out2 and lse;
  *   d: 64 or 128 (32 or 64 columns per map); scale: finite and positive;
  *   tile: th * tw divides 128 and tt is a multiple of 128 / (th * tw);
- *   window_per_head: host array of `heads` entries, heads <= 256;
- *   workspace: device memory of at least
- *     sta_diff_attention_fwd_workspace(...) bytes (0 for short windows: may then
- *     be NULL), 16-byte aligned, used until the call's kernels have run.  Calls
- *     that may overlap on the GPU, and graphs that may run at the same time,
- *     need a workspace each.
+ *   window_per_head: host array of `heads` entries, heads <= 256.
  * The first library call on a device allocates the status word; make it before
  * any stream capture.  batch = 0 or heads = 0 is a no-op.
  * Errors: NULL, ALIGN, ALIAS (an output overlaps another buffer), SHAPE, WINDOW,
- * HEADDIM, ARG, SCRATCH, ARCH, CUDA.
+ * HEADDIM, ARG, ARCH, CUDA.
  */
 sta_status sta_diff_attention_fwd(const void* q, const void* k, const void* v, const float* lambda, void* out,
                                   void* out2, float* lse, int32_t batch, int32_t heads, int32_t d,
                                   int32_t token_major, sta_dim3 grid, sta_dim3 tile,
-                                  const sta_dim3* window_per_head, float scale, void* workspace,
-                                  int64_t workspace_bytes, void* stream);
-
-/* Bytes of workspace sta_diff_attention_fwd needs (host only), or -1 on an invalid argument. */
-int64_t sta_diff_attention_fwd_workspace(int32_t batch, int32_t heads, int32_t d, sta_dim3 grid, sta_dim3 tile,
-                                         const sta_dim3* window_per_head);
+                                  const sta_dim3* window_per_head, float scale, void* stream);
 
 /*
  * Backward of sta_diff_attention_fwd, with out, out2 and lse as it wrote them and
@@ -366,7 +356,10 @@ int64_t sta_diff_attention_fwd_workspace(int32_t batch, int32_t heads, int32_t d
  * P is rebuilt from lse; the products take P and dS rounded to bf16 and accumulate
  * in fp32.  dq, dk, dv: device bf16 laid out like q; dlambda: device fp32 [heads].
  * Every output element is written.  Deterministic: no atomics.
- * workspace as above, sta_diff_attention_bwd_workspace(...) bytes.
+ *   workspace: device memory of at least sta_diff_attention_bwd_workspace(...) bytes,
+ *     16-byte aligned, used until the call's kernels have run.  Calls that may overlap
+ *     on the GPU, and graphs that may run at the same time, need a workspace each.
+ * Errors: as the forward, and SCRATCH.
  */
 sta_status sta_diff_attention_bwd(const void* q, const void* k, const void* v, const float* lambda, const void* out,
                                   const void* out2, const float* lse, const void* dout, void* dq, void* dk, void* dv,
@@ -374,6 +367,7 @@ sta_status sta_diff_attention_bwd(const void* q, const void* k, const void* v, c
                                   sta_dim3 grid, sta_dim3 tile, const sta_dim3* window_per_head, float scale,
                                   void* workspace, int64_t workspace_bytes, void* stream);
 
+/* Bytes of workspace sta_diff_attention_bwd needs (host only), or -1 on an invalid argument. */
 int64_t sta_diff_attention_bwd_workspace(int32_t batch, int32_t heads, int32_t d, sta_dim3 grid, sta_dim3 tile,
                                          const sta_dim3* window_per_head);
 

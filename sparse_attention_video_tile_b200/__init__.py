@@ -68,9 +68,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "sta_forward_host": (ctypes.c_int, [P, P, P, P, I32, I32, I32, D3, D3, ctypes.POINTER(D3), F, I32, P]),
         "sta_attention_fwd_lse": (ctypes.c_int, [P, P, P, P, P, I32, I32, I32, D3, D3, ctypes.POINTER(D3), F, P]),
         "sta_attention_bwd": (ctypes.c_int, [P, P, P, P, P, P, P, P, P, I32, I32, I32, D3, D3, ctypes.POINTER(D3), F, P]),
-        "sta_diff_attention_fwd": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I32, I32, D3, D3, ctypes.POINTER(D3), F,
-                                                  P, I64, P]),
-        "sta_diff_attention_fwd_workspace": (I64, [I32, I32, I32, D3, D3, ctypes.POINTER(D3)]),
+        "sta_diff_attention_fwd": (ctypes.c_int, [P, P, P, P, P, P, P, I32, I32, I32, I32, D3, D3, ctypes.POINTER(D3), F, P]),
         "sta_diff_attention_bwd": (ctypes.c_int, [P] * 12 + [I32, I32, I32, I32, D3, D3, ctypes.POINTER(D3), F, P, I64, P]),
         "sta_diff_attention_bwd_workspace": (I64, [I32, I32, I32, D3, D3, ctypes.POINTER(D3)]),
         "sta_layer_norm_fwd": (ctypes.c_int, [P] * 8 + [I64, I32, I32, I32, F, F, P, P]),
@@ -574,9 +572,8 @@ def _forward_from_host_chunks(q_h, k_h, v_h, out_h, grid, tile, window_per_head,
 # The operators around an attention block (block.py) are reached through the package too;
 # they are imported on first use, since that module needs torch at import.
 _BLOCK = frozenset((
-    "sta_diff_attention_bwd", "sta_diff_attention_bwd_workspace", "sta_diff_attention_fwd",
-    "sta_diff_attention_fwd_workspace", "sta_diff_forward", "sta_dropout", "sta_dropout_forward",
-    "sta_layer_norm_backward", "sta_layer_norm_bwd", "sta_layer_norm_bwd_workspace", "sta_layer_norm_forward",
+    "sta_diff_attention_bwd", "sta_diff_attention_bwd_workspace", "sta_diff_attention_fwd", "sta_diff_forward",
+    "sta_dropout", "sta_dropout_forward", "sta_layer_norm_backward", "sta_layer_norm_bwd", "sta_layer_norm_bwd_workspace", "sta_layer_norm_forward",
     "sta_layer_norm_fwd"))
 
 

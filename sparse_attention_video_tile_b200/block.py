@@ -239,50 +239,33 @@ def _diff_dims(q, grid, token_major: bool, windows):
     return B, Hn, L, d
 
 
-def _diff_workspace(which: str, q, grid, tile, windows, token_major: bool) -> int:
-    B, Hn, _, d = _diff_dims(q, grid, token_major, windows)
-    n = getattr(load_library(), which)(B, Hn, d, *_geometry(grid, tile, windows))
+def sta_diff_attention_bwd_workspace(q, grid, tile, window_per_head, token_major: bool = False) -> int:
+    """Bytes of workspace that ``sta_diff_attention_bwd`` needs for tensors shaped like q."""
+    B, Hn, _, d = _diff_dims(q, grid, token_major, window_per_head)
+    n = load_library().sta_diff_attention_bwd_workspace(B, Hn, d, *_geometry(grid, tile, window_per_head))
     if n < 0:
-        raise StaError(10, which)
+        raise StaError(10, "sta_diff_attention_bwd_workspace")
     return int(n)
 
 
-def sta_diff_attention_fwd_workspace(q, grid, tile, window_per_head, token_major: bool = False) -> int:
-    """Bytes of workspace that ``sta_diff_attention_fwd`` needs for tensors shaped like q."""
-    return _diff_workspace("sta_diff_attention_fwd_workspace", q, grid, tile, window_per_head, token_major)
-
-
-def sta_diff_attention_bwd_workspace(q, grid, tile, window_per_head, token_major: bool = False) -> int:
-    """Bytes of workspace that ``sta_diff_attention_bwd`` needs for tensors shaped like q."""
-    return _diff_workspace("sta_diff_attention_bwd_workspace", q, grid, tile, window_per_head, token_major)
-
-
 def sta_diff_attention_fwd(q, k, v, lam, out, grid, tile, window_per_head: Sequence, scale: float, out2=None, lse=None,
-                           token_major: bool = False, workspace=None, stream=None) -> None:
+                           token_major: bool = False, stream=None) -> None:
     """Differential attention over tile windows on raster-order bf16 CUDA tensors
     [B, heads, T*H*W, d] ([B, T*H*W, heads, d] with ``token_major``):
     out = (softmax(scale Q1 K1^T) - lam softmax(scale Q2 K2^T)) V, where Q1, K1 are the
     first d/2 columns of q and k, Q2, K2 the last d/2, and lam is fp32 [heads].
     ``out2`` (shaped like out) receives softmax(scale Q2 K2^T) V and ``lse`` (fp32
-    [2, B, heads, L]) both maps' log-sum-exps, which the backward needs.
-    ``workspace`` (at least ``sta_diff_attention_fwd_workspace`` bytes) is allocated
-    when it is None."""
+    [2, B, heads, L]) both maps' log-sum-exps, which the backward needs."""
     B, Hn, L, d = _diff_dims(q, grid, token_major, window_per_head)
     geo = _geometry(grid, tile, window_per_head)
-    with _On(stream, q, k, v, lam, out, out2, lse, workspace) as st:
+    with _On(stream, q, k, v, lam, out, out2, lse) as st:
         shape = q.shape
         ptrs = [_ptr(q, "q", torch.bfloat16)] + [_ptr(t, n, torch.bfloat16, shape) for n, t in (("k", k), ("v", v))]
         ptrs.append(_ptr(lam, "lam", torch.float32, (Hn,)))
         ptrs.append(_ptr(out, "out", torch.bfloat16, shape))
         ptrs.append(_ptr(out2, "out2", torch.bfloat16, shape, optional=True))
         ptrs.append(_ptr(lse, "lse", torch.float32, (2, B, Hn, L), optional=True))
-        if workspace is None:
-            need = load_library().sta_diff_attention_fwd_workspace(B, Hn, d, *geo)
-            if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        pw, nw = _workspace_ptr(workspace, "workspace")
-        _check(load_library().sta_diff_attention_fwd(*ptrs, B, Hn, d, int(bool(token_major)), *geo, float(scale), pw, nw,
-                                                     st),
+        _check(load_library().sta_diff_attention_fwd(*ptrs, B, Hn, d, int(bool(token_major)), *geo, float(scale), st),
                "sta_diff_attention_fwd")
 
 
@@ -321,5 +304,5 @@ def sta_diff_forward(q, k, v, lam, grid, tile, window_per_head: Sequence, scale:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         out2 = torch.empty_like(out) if save else None
         lse = torch.empty((2, B, Hn, L), dtype=torch.float32, device=q.device) if save else None
-    sta_diff_attention_fwd(q, k, v, lam, out, grid, tile, window_per_head, sc, out2, lse, token_major, None, stream)
+    sta_diff_attention_fwd(q, k, v, lam, out, grid, tile, window_per_head, sc, out2, lse, token_major, stream)
     return (out, out2, lse) if save else out

@@ -93,8 +93,6 @@ int64_t copy_bytes(const DiffGeo& g, int32_t d) {
   return round256(static_cast<int64_t>(g.batch) * g.heads * g.Lpad * d * 2);
 }
 
-int64_t fwd_bytes(const DiffGeo& g, int32_t d) { return diff_fwd_copies(g, d) ? 2 * copy_bytes(g, d) : 0; }
-
 // Backward workspace: tiled q, k, v, dout; four row vectors; parts of dlambda.
 struct BwdLayout {
   int64_t vec, part, total;
@@ -120,12 +118,6 @@ using namespace sta;
 
 extern "C" {
 
-int64_t sta_diff_attention_fwd_workspace(int32_t batch, int32_t heads, int32_t d, sta_dim3 grid, sta_dim3 tile,
-                                         const sta_dim3* window_per_head) {
-  DiffGeo g;
-  return make_diff_geo(batch, heads, d, 0, grid, tile, window_per_head, &g) == STA_OK ? fwd_bytes(g, d) : -1;
-}
-
 int64_t sta_diff_attention_bwd_workspace(int32_t batch, int32_t heads, int32_t d, sta_dim3 grid, sta_dim3 tile,
                                          const sta_dim3* window_per_head) {
   DiffGeo g;
@@ -135,8 +127,7 @@ int64_t sta_diff_attention_bwd_workspace(int32_t batch, int32_t heads, int32_t d
 sta_status sta_diff_attention_fwd(const void* q, const void* k, const void* v, const float* lambda, void* out,
                                   void* out2, float* lse, int32_t batch, int32_t heads, int32_t d,
                                   int32_t token_major, sta_dim3 grid, sta_dim3 tile,
-                                  const sta_dim3* window_per_head, float scale, void* workspace,
-                                  int64_t workspace_bytes, void* stream) {
+                                  const sta_dim3* window_per_head, float scale, void* stream) {
   DiffGeo g;
   sta_status s = make_diff_geo(batch, heads, d, token_major, grid, tile, window_per_head, &g);
   if (s != STA_OK) return s;
@@ -144,24 +135,18 @@ sta_status sta_diff_attention_fwd(const void* q, const void* k, const void* v, c
   const int64_t bh = static_cast<int64_t>(batch) * heads;
   if (bh == 0) return STA_OK;
   if (!q || !k || !v || !lambda || !out) return STA_ERR_NULL;
-  for (const void* p : {q, k, v, static_cast<const void*>(out), static_cast<const void*>(out2),
-                        static_cast<const void*>(workspace)})
+  for (const void* p : {q, k, v, static_cast<const void*>(out), static_cast<const void*>(out2)})
     if (!aligned16(p)) return STA_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(lse) % 4 != 0 || reinterpret_cast<uintptr_t>(lambda) % 4 != 0) return STA_ERR_ALIGN;
-  const int64_t need = fwd_bytes(g, d);
-  if (need > 0 && !workspace) return STA_ERR_NULL;
-  if (need > 0 && workspace_bytes < need) return STA_ERR_SCRATCH;
   const int64_t n = bh * g.L * d * 2;
-  const Range r[] = {{out, n}, {out2, n}, {lse, 2 * bh * g.L * 4}, {workspace, need}, {q, n}, {k, n}, {v, n},
-                     {lambda, heads * 4}};
-  if (any_overlap(r, 4, 8)) return STA_ERR_ALIAS;
+  const Range r[] = {{out, n}, {out2, n}, {lse, 2 * bh * g.L * 4}, {q, n}, {k, n}, {v, n}, {lambda, heads * 4}};
+  if (any_overlap(r, 3, 7)) return STA_ERR_ALIAS;
   int dev = 0;
   int32_t* err = nullptr;
   if ((s = check_device(&dev)) != STA_OK || (s = status_word(dev, &err)) != STA_OK) return s;
   DiffFwdArgs a{};
   a.q = q; a.k = k; a.v = v; a.lam = lambda;
   a.out = out; a.out2 = out2; a.lse = lse;
-  a.tiled = need > 0 ? workspace : nullptr;
   a.d = d;
   a.scale = scale;
   const cudaError_t e = launch_diff_fwd(g, a, err, kWaitLimitNs, static_cast<cudaStream_t>(stream));

@@ -38,7 +38,6 @@ struct DiffFwdArgs {
   const float* lam;
   void *out, *out2;
   float* lse;
-  void* tiled;                 // k and v in the tiled order of the padded latent, or null: read them in place
   int32_t d;
   float scale;
 };
@@ -54,9 +53,6 @@ struct DiffBwdArgs {
   int32_t d;
   float scale;
 };
-
-// Whether the forward copies k and v into tiled order first (needs the workspace).
-bool diff_fwd_copies(const DiffGeo& g, int32_t d);
 
 cudaError_t launch_diff_fwd(const DiffGeo& g, const DiffFwdArgs& a, int32_t* err, uint64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_diff_bwd(const DiffGeo& g, const DiffBwdArgs& a, int32_t* err, uint64_t limit_ns, cudaStream_t stream);

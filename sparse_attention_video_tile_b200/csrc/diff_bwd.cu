@@ -774,7 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(sb + S::kLEmpty);
-        ok = __all_sync(0xffffffffu, mbar_wait(sb + S::kPFull, seq & 1, wc, 0x4c) && mbar_wait(sb + S::kDFull, seq & 1, wc, 0x4d));
+        ok = __all_sync(0xffffffffu, mbar_wait(sb + S::kPFull, seq & 1, wc, 0x4c) &&
+                                         mbar_wait(sb + S::kDFull, seq & 1, wc, 0x4d));
         if (!ok) break;
         tc_fence_after();
         uint32_t d2[32];

@@ -76,7 +76,6 @@ struct FwdParams {
   __nv_bfloat16 *out, *out2;
   float* lse;
   int32_t n_items;
-  int32_t kv_tiled;
   float scale_log2;
   int32_t* err;
   uint64_t limit_ns;
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(sb + S::kKEmpty + 8 * st, ((seq / KS) & 1) ^ 1, wc, 0x22);
           if (!ok) break;
           mbar_arrive_expect_tx(sb + S::kKFull + 8 * st, S::kBlk);
-          load_block<D>(g, sb + S::kK + st * S::kBlk, &tm_k, sb + S::kKFull + 8 * st, it, b, p.kv_tiled != 0);
+          load_block<D>(g, sb + S::kK + st * S::kBlk, &tm_k, sb + S::kKFull + 8 * st, it, b, false);
         }
         if (!ok) {   // this item's Q is in flight
           ++k;
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(sb + S::kVEmpty + 8 * st, ((seq / KS) & 1) ^ 1, wc, 0x23);
           if (!ok) break;
           mbar_arrive_expect_tx(sb + S::kVFull + 8 * st, S::kBlk);
-          load_block<D>(g, sb + S::kV + st * S::kBlk, &tm_v, sb + S::kVFull + 8 * st, it, b, p.kv_tiled != 0);
+          load_block<D>(g, sb + S::kV + st * S::kBlk, &tm_v, sb + S::kVFull + 8 * st, it, b, false);
         }
       }
       for (uint32_t i = 0; i < KS && i < seq; ++i) {
@@ -422,64 +421,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kPvWarp) tmem_dealloc(tmem, 512);
 }
 
-// Raster k, v -> tiled order of the padded latent, pad rows zero (blockIdx.y: tensor).
-// D / 8 threads move a row, 16 bytes each.
-template <int D>
-__global__ void __launch_bounds__(256) diff_copy_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
-                                                        uint4* __restrict__ dst, const __grid_constant__ DiffGeo g) {
-  constexpr int C = D / 8, U = 4;
-  const int64_t rows = static_cast<int64_t>(g.batch) * g.heads * g.Lpad;
-  const uint4* src = blockIdx.y == 0 ? k : v;
-  uint4* out = dst + static_cast<int64_t>(blockIdx.y) * rows * C;
-  const int c = static_cast<int>(threadIdx.x) % C;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * (256 / C * U) + threadIdx.x / C;
-  const int32_t plane = g.th * g.tw;
-  uint4 val[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t r = r0 + u * (256 / C);
-    val[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows) {
-      const int32_t bh = static_cast<int32_t>(r / g.Lpad), x = static_cast<int32_t>(r - bh * g.Lpad);
-      const int32_t tile = x / g.ntile, i = x - tile * g.ntile;
-      const Block b{tile / (g.nH * g.nW), (tile / g.nW) % g.nH, tile % g.nW, 0};
-      const int32_t token = token_of(g, b, Local{i / plane, (i % plane) / g.tw, i % g.tw});
-      if (token >= 0) val[u] = __ldg(src + row_of(g, bh / g.heads, bh % g.heads, token) * C + c);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t r = r0 + u * (256 / C);
-    if (r < rows) out[r * C + c] = val[u];
-  }
-}
-
 template <int D, bool PAD>
 cudaError_t launch_t(const DiffGeo& g, const DiffFwdArgs& a, int32_t* err, uint64_t limit_ns, cudaStream_t stream) {
   using S = Fwd<D>;
   const int64_t bh = static_cast<int64_t>(g.batch) * g.heads;
-  const __nv_bfloat16* kt = static_cast<const __nv_bfloat16*>(a.tiled);
   // before the tensor maps: makes the device's context current in a thread that has not
   // used the device yet, which the driver's encode call needs
   auto kern = diff_fwd_kernel<D, PAD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
   CUtensorMap tq, tk, tv;
-  bool ok = map_raster(&tq, a.q, g, D);
-  if (a.tiled)
-    ok = ok && map_tiled(&tk, kt, g, D) && map_tiled(&tv, kt + bh * g.Lpad * D, g, D);
-  else
-    ok = ok && map_raster(&tk, a.k, g, D) && map_raster(&tv, a.v, g, D);
-  if (!ok) return cudaErrorInvalidValue;
+  if (!map_raster(&tq, a.q, g, D) || !map_raster(&tk, a.k, g, D) || !map_raster(&tv, a.v, g, D))
+    return cudaErrorInvalidValue;
   int sms = 0;
   if ((e = sm_count(&sms)) != cudaSuccess) return e;
-  if (a.tiled) {
-    const int64_t per = 256 / (D / 8) * 4, blocks = (bh * g.Lpad + per - 1) / per;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    diff_copy_kernel<D><<<dim3(static_cast<unsigned>(blocks), 2), 256, 0, stream>>>(
-        static_cast<const uint4*>(a.k), static_cast<const uint4*>(a.v), static_cast<uint4*>(a.tiled), g);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
   FwdParams p;
   p.g = g;
   p.lam = a.lam;
@@ -487,7 +442,6 @@ cudaError_t launch_t(const DiffGeo& g, const DiffFwdArgs& a, int32_t* err, uint6
   p.out2 = static_cast<__nv_bfloat16*>(a.out2);
   p.lse = a.lse;
   p.n_items = static_cast<int32_t>(bh * g.blocks);
-  p.kv_tiled = a.tiled != nullptr;
   p.scale_log2 = a.scale * kLog2e;
   p.err = err;
   p.limit_ns = limit_ns;
@@ -496,12 +450,6 @@ cudaError_t launch_t(const DiffGeo& g, const DiffFwdArgs& a, int32_t* err, uint6
 }
 
 }  // namespace
-
-bool diff_fwd_copies(const DiffGeo& g, int32_t d) {
-  (void)g;
-  (void)d;
-  return false;
-}
 
 cudaError_t launch_diff_fwd(const DiffGeo& g, const DiffFwdArgs& a, int32_t* err, uint64_t limit_ns, cudaStream_t stream) {
   if (a.d == 128)

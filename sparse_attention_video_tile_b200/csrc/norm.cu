@@ -21,7 +21,6 @@ using namespace norm;
 // registers: with the next rows prefetched into registers the kernel moved 3.8 TB/s.
 template <typename T, int TPR, int CH, int R, int STAGES>
 __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const NormFwdArgs a) {
-  constexpr bool VEC = false;
   constexpr bool kBlock = TPR == 0;
   constexpr bool kKeep = CH <= 2 && !kBlock;      // weight and bias stay in registers
   constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
@@ -56,9 +55,9 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
         b[k][i] = 0;
       }
       if (ch < n8) {
-        const int n = VEC ? 8 : min(8, a.cols - ch * 8);
-        if (a.weight != nullptr) load_param2<T, VEC>(a.weight, a.wfp32, ch * 8, n, w[k]);
-        if (a.bias != nullptr) load_param2<T, VEC>(a.bias, a.wfp32, ch * 8, n, b[k]);
+        const int n = min(8, a.cols - ch * 8);
+        if (a.weight != nullptr) load_param2<T>(a.weight, a.wfp32, ch * 8, n, w[k]);
+        if (a.bias != nullptr) load_param2<T>(a.bias, a.wfp32, ch * 8, n, b[k]);
       }
     }
   }
@@ -89,7 +88,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int q = r * kGroups + grp, c0 = (lane + k * step) * 8;
-        span_get<T, VEC>(ex, q * a.cols + c0, q < live ? a.cols - c0 : 0, f[r][k]);
+        span_get<T>(ex, q * a.cols + c0, q < live ? a.cols - c0 : 0, f[r][k]);
       }
     if (a.drop.thr > 0) {
 #pragma unroll
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
         for (int k = 0; k < CH; ++k) {
           const int q = r * kGroups + grp, c0 = (lane + k * step) * 8;
           uint64_t g[4];
-          span_get<T, VEC>(er, q * a.cols + c0, q < live ? a.cols - c0 : 0, g);
+          span_get<T>(er, q * a.cols + c0, q < live ? a.cols - c0 : 0, g);
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[r][k][i] = add_f32x2(f[r][k][i], g[i]);
         }
@@ -128,13 +127,13 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int32_t left = a.cols - (lane + k * step) * 8;   // columns of the chunk that exist
-        if (VEC ? left > 0 : left >= 8) {
+        if (left >= 8) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint64_t e = add_f32x2(f[r][k][i], nm);
             s[i & 1] = fma_f32x2(e, e, s[i & 1]);
           }
-        } else if (!VEC) {
+        } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float u, v;
@@ -151,13 +150,13 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
     for (int out = 0; out < 2; ++out) {
       T* dst = out == 0 ? h : y;
       if (dst == nullptr) continue;
-      if (!VEC) span_sync<kBlock>();   // the slot's values are in registers (or stored): it carries the output
+      span_sync<kBlock>();   // the slot's values are in registers (or stored): it carries the output
       T* eo = span_elems(p, dst + base * a.cols);
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int32_t ch = lane + k * step;
         if (ch >= n8) continue;
-        const int n = VEC ? 8 : min(8, a.cols - ch * 8);
+        const int n = min(8, a.cols - ch * 8);
         uint64_t wk[4], bk[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -165,8 +164,8 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
           bk[i] = kKeep ? b[kKeep ? k : 0][i] : 0;
         }
         if (!kKeep && out == 1) {
-          if (a.weight != nullptr) load_param2<T, VEC>(a.weight, a.wfp32, ch * 8, n, wk);
-          if (a.bias != nullptr) load_param2<T, VEC>(a.bias, a.wfp32, ch * 8, n, bk);
+          if (a.weight != nullptr) load_param2<T>(a.weight, a.wfp32, ch * 8, n, wk);
+          if (a.bias != nullptr) load_param2<T>(a.bias, a.wfp32, ch * 8, n, bk);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -177,25 +176,17 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             v[i] = out == 0 ? f[r][k][i] : fma_f32x2(mul_f32x2(add_f32x2(f[r][k][i], nm), rs), wk[i], bk[i]);
-          if constexpr (VEC) {
-            Chunk<T> o;
-            o.put2(v);
-            o.store(dst + (base + q) * a.cols + ch * 8);
-          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float u, t;
-              f32x2_split(v[i], u, t);
-              if (2 * i < n) eo[q * a.cols + ch * 8 + 2 * i] = from_f<T>(u);
-              if (2 * i + 1 < n) eo[q * a.cols + ch * 8 + 2 * i + 1] = from_f<T>(t);
-            }
+          for (int i = 0; i < 4; ++i) {
+            float u, t;
+            f32x2_split(v[i], u, t);
+            if (2 * i < n) eo[q * a.cols + ch * 8 + 2 * i] = from_f<T>(u);
+            if (2 * i + 1 < n) eo[q * a.cols + ch * 8 + 2 * i + 1] = from_f<T>(t);
           }
         }
       }
-      if (!VEC) {
-        span_sync<kBlock>();
-        span_store(p, dst + base * a.cols, live * a.cols, st, snt);
-      }
+      span_sync<kBlock>();
+      span_store(p, dst + base * a.cols, live * a.cols, st, snt);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -238,6 +229,9 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 ? 2 : 1) norm_fwd
   PhiloxKey key{};
   if (DROP) key = philox_key(a.drop.rng);
   const float inv_n = 1.0f / static_cast<float>(a.cols);
+  const int psize = a.wfp32 ? 4 : static_cast<int>(sizeof(T)), p_bytes = step * 8 * psize;
+  const char* wp = static_cast<const char*>(a.weight) + lane * 8 * psize;   // this thread's first parameters
+  const char* bp = static_cast<const char*>(a.bias) + lane * 8 * psize;
   uint64_t w[kKeep ? CH : 1][4], b[kKeep ? CH : 1][4];
   if constexpr (kKeep) {
 #pragma unroll
@@ -249,8 +243,8 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 ? 2 : 1) norm_fwd
         b[k][i] = 0;
       }
       if (ch < n8) {
-        if (a.weight != nullptr) load_param2<T, true>(a.weight, a.wfp32, ch * 8, 8, w[k]);
-        if (a.bias != nullptr) load_param2<T, true>(a.bias, a.wfp32, ch * 8, 8, b[k]);
+        if (a.weight != nullptr) read_param2<T>(wp + k * p_bytes, a.wfp32, w[k]);
+        if (a.bias != nullptr) read_param2<T>(bp + k * p_bytes, a.wfp32, b[k]);
       }
     }
   }
@@ -262,8 +256,6 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 ? 2 : 1) norm_fwd
   const int k_bytes = step * kChunkBytes;
   const int64_t row0 = unit * kRows + grp, off0 = row0 * row_bytes + lane * kChunkBytes;
   const int64_t step_rows = units * kRows;
-  const int psize = a.wfp32 ? 4 : static_cast<int>(sizeof(T)), p_bytes = step * 8 * psize;
-  const char *wp = static_cast<const char*>(a.weight) + lane * 8 * psize, *bp = static_cast<const char*>(a.bias) + lane * 8 * psize;
   const char* px = static_cast<const char*>(a.x) + off0;
   const char* pr = static_cast<const char*>(a.residual) + off0;
   int64_t left_in = a.rows - row0;
@@ -387,7 +379,8 @@ template <typename T, bool VEC, int TPR, int CH, int R, int STAGES>
 cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t stream) {
   void (*kern)(NormFwdArgs);
   if constexpr (VEC)
-    kern = a.drop.thr > 0 ? norm_fwd_vec_kernel<T, true, TPR, CH, R, STAGES> : norm_fwd_vec_kernel<T, false, TPR, CH, R, STAGES>;
+    kern = a.drop.thr > 0 ? norm_fwd_vec_kernel<T, true, TPR, CH, R, STAGES>
+                          : norm_fwd_vec_kernel<T, false, TPR, CH, R, STAGES>;
   else
     kern = norm_fwd_kernel<T, TPR, CH, R, STAGES>;
   constexpr int rows = (TPR > 0 ? 32 / (TPR > 0 ? TPR : 1) : 1) * R;   // of a warp's (block's) step

@@ -47,7 +47,6 @@ __device__ __forceinline__ void row_sum2(float& u, float& v, float2* red) {
 // time, while the next STAGES - 1 steps of its warp (block) are on their way to shared memory.
 template <typename T, int TPR, int CH, int R, int STAGES>
 __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const NormBwdArgs a) {
-  constexpr bool VEC = false;
   constexpr bool kBlock = TPR == 0;
   constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
   constexpr int kRows = kGroups * R;   // rows of a warp's (block's) step
@@ -80,7 +79,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
       db[k][i] = 0;
     }
     if (a.weight != nullptr && ch < n8)
-      load_param2<T, VEC>(a.weight, a.wfp32, ch * 8, VEC ? 8 : min(8, a.cols - ch * 8), w[k]);
+      load_param2<T>(a.weight, a.wfp32, ch * 8, min(8, a.cols - ch * 8), w[k]);
   }
   const float inv_n = 1.0f / static_cast<float>(a.cols);
   auto rows_at = [&](int64_t base) { return static_cast<int>(min(static_cast<int64_t>(kRows), a.rows - base)); };
@@ -127,8 +126,8 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int c0 = (lane + k * step) * 8, e0 = q * a.cols + c0, n = q < live ? a.cols - c0 : 0;
-        span_get<T, VEC>(ey, e0, n, g[r][k]);
-        span_get<T, VEC>(ez, e0, n, z[r][k]);
+        span_get<T>(ey, e0, n, g[r][k]);
+        span_get<T>(ez, e0, n, z[r][k]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint64_t y = g[r][k][i];
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
         if (dh != nullptr) {
           const int q = r * kGroups + grp, c0 = (lane + k * step) * 8;
           uint64_t d2[4];
-          span_get<T, VEC>(ed, q * a.cols + c0, q < live ? a.cols - c0 : 0, d2);
+          span_get<T>(ed, q * a.cols + c0, q < live ? a.cols - c0 : 0, d2);
 #pragma unroll
           for (int i = 0; i < 4; ++i) g[r][k][i] = add_f32x2(g[r][k][i], d2[i]);
         }
@@ -169,7 +168,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
     for (int out = 0; out < 2; ++out) {
       T* dst = static_cast<T*>(out == 0 ? a.dres : a.dx);
       if (dst == nullptr) continue;
-      if (!VEC) span_sync<kBlock>();   // the slot's values are in registers (or stored): it carries the output
+      span_sync<kBlock>();   // the slot's values are in registers (or stored): it carries the output
       T* eo = span_elems(p, dst + base * a.cols);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -183,26 +182,18 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = g[r][k][i];
           if (out == 1 && a.drop.thr > 0) drop_pairs(v, static_cast<uint64_t>(base + q) * n8 + ch, key, a.drop);
-          if constexpr (VEC) {
-            Chunk<T> o;
-            o.put2(v);
-            o.store(dst + (base + q) * a.cols + ch * 8);
-          } else {
-            const int n = min(8, a.cols - ch * 8);
+          const int n = min(8, a.cols - ch * 8);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float u, t;
-              f32x2_split(v[i], u, t);
-              if (2 * i < n) eo[q * a.cols + ch * 8 + 2 * i] = from_f<T>(u);
-              if (2 * i + 1 < n) eo[q * a.cols + ch * 8 + 2 * i + 1] = from_f<T>(t);
-            }
+          for (int i = 0; i < 4; ++i) {
+            float u, t;
+            f32x2_split(v[i], u, t);
+            if (2 * i < n) eo[q * a.cols + ch * 8 + 2 * i] = from_f<T>(u);
+            if (2 * i + 1 < n) eo[q * a.cols + ch * 8 + 2 * i + 1] = from_f<T>(t);
           }
         }
       }
-      if (!VEC) {
-        span_sync<kBlock>();
-        span_store(p, dst + base * a.cols, live * a.cols, st, snt);
-      }
+      span_sync<kBlock>();
+      span_store(p, dst + base * a.cols, live * a.cols, st, snt);
     }
     span_sync<kBlock>();   // every thread is done with the slot: the next step's fetch fills it
     slot = slot + 1 == STAGES ? 0 : slot + 1;
@@ -293,7 +284,8 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 ? 2 : 1) norm_bwd
       dw[k][i] = 0;
       db[k][i] = 0;
     }
-    if (a.weight != nullptr && ch < n8) load_param2<T, true>(a.weight, a.wfp32, ch * 8, 8, w[k]);
+    if (a.weight != nullptr && ch < n8)
+      read_param2<T>(static_cast<const char*>(a.weight) + ch * (a.wfp32 ? 32 : 8 * static_cast<int>(sizeof(T))), a.wfp32, w[k]);
   }
   const float inv_n = 1.0f / static_cast<float>(a.cols);
   const int64_t row_bytes = static_cast<int64_t>(a.cols) * sizeof(T);
@@ -518,7 +510,8 @@ template <typename T, bool VEC, int TPR, int CH, int R, int STAGES>
 cudaError_t launch_bwd(const NormBwdArgs& a, const BwdShape& s, cudaStream_t stream) {
   void (*kern)(NormBwdArgs);
   if constexpr (VEC)
-    kern = a.drop.thr > 0 ? norm_bwd_vec_kernel<T, true, TPR, CH, R, STAGES> : norm_bwd_vec_kernel<T, false, TPR, CH, R, STAGES>;
+    kern = a.drop.thr > 0 ? norm_bwd_vec_kernel<T, true, TPR, CH, R, STAGES>
+                          : norm_bwd_vec_kernel<T, false, TPR, CH, R, STAGES>;
   else
     kern = norm_bwd_kernel<T, TPR, CH, R, STAGES>;
   constexpr int rows = (TPR > 0 ? 32 / (TPR > 0 ? TPR : 1) : 1) * R;

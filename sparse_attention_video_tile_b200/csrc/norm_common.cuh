@@ -222,22 +222,11 @@ __device__ __forceinline__ void span_store(const uint8_t* buf, T* g, int n, int 
   }
 }
 // Eight elements of a span from e0 on, as pairs of fp32; those from n on read as zero.
-template <typename T, bool VEC>
+template <typename T>
 __device__ __forceinline__ void span_get(const T* e, int e0, int n, uint64_t (&f)[4]) {
-  if constexpr (VEC) {
-    Chunk<T> c;
-    const uint4* q = reinterpret_cast<const uint4*>(e + e0);
 #pragma unroll
-    for (int i = 0; i < Chunk<T>::kWords / 4; ++i) {
-      const uint4 v = n > 0 ? q[i] : make_uint4(0u, 0u, 0u, 0u);
-      c.w[4 * i] = v.x; c.w[4 * i + 1] = v.y; c.w[4 * i + 2] = v.z; c.w[4 * i + 3] = v.w;
-    }
-    c.get2(f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f[i] = f32x2(2 * i < n ? to_f<T>(e[e0 + 2 * i]) : 0.f, 2 * i + 1 < n ? to_f<T>(e[e0 + 2 * i + 1]) : 0.f);
-  }
+  for (int i = 0; i < 4; ++i)
+    f[i] = f32x2(2 * i < n ? to_f<T>(e[e0 + 2 * i]) : 0.f, 2 * i + 1 < n ? to_f<T>(e[e0 + 2 * i + 1]) : 0.f);
 }
 // Pairs through the dropout mask.  Dropped values are replaced, not multiplied by zero: an
 // infinity or NaN there stays out.
@@ -294,32 +283,6 @@ __device__ __forceinline__ void span_sync() {
   if (BLOCK) __syncthreads(); else __syncwarp();
 }
 
-// Columns c .. c + 7 of the weight or bias as fp32 (n of them exist; the rest read as zero).
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_param(const void* p, bool fp32, int32_t c, int n, float (&f)[8]) {
-  if constexpr (VEC) {
-    if (fp32) {
-      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
-      const float4 a = __ldg(q), b = __ldg(q + 1);
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else {
-      Chunk<T> k;
-      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c);
-#pragma unroll
-      for (int i = 0; i < Chunk<T>::kWords / 4; ++i) {
-        const uint4 v = __ldg(q + i);
-        k.w[4 * i] = v.x; k.w[4 * i + 1] = v.y; k.w[4 * i + 2] = v.z; k.w[4 * i + 3] = v.w;
-      }
-      k.get(f);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      f[i] = i < n ? (fp32 ? static_cast<const float*>(p)[c + i] : to_f<T>(static_cast<const T*>(p)[c + i])) : 0.f;
-  }
-}
-
 // The eight parameters at p, an address in an array of `fp32` or T elements.
 template <typename T>
 __device__ __forceinline__ void read_param2(const char* p, bool fp32, uint64_t (&f)[4]) {
@@ -339,10 +302,13 @@ __device__ __forceinline__ void read_param2(const char* p, bool fp32, uint64_t (
     k.get2(f);
   }
 }
-template <typename T, bool VEC>
+// Parameters c .. c + 7 of the weight or bias, n of which exist (the rest read as zero).
+template <typename T>
 __device__ __forceinline__ void load_param2(const void* p, bool fp32, int32_t c, int n, uint64_t (&f)[4]) {
   float v[8];
-  load_param<T, VEC>(p, fp32, c, n, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = i < n ? (fp32 ? static_cast<const float*>(p)[c + i] : to_f<T>(static_cast<const T*>(p)[c + i])) : 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = f32x2(v[2 * i], v[2 * i + 1]);
 }

@@ -210,7 +210,6 @@ def test_from_threads_that_have_not_used_the_device():
 
 def test_nothing_outside_the_outputs_is_written():
     q, k, v, do, lam = inputs(12)
-    need_f = sta.sta_diff_attention_fwd_workspace(q, GRID, TILE, WINDOWS)
     need_b = sta.sta_diff_attention_bwd_workspace(q, GRID, TILE, WINDOWS)
 
     def guarded(numel, dtype):
@@ -221,16 +220,16 @@ def test_nothing_outside_the_outputs_is_written():
     bufs["lse"] = guarded(2 * q.numel() // 64, torch.float32)
     bufs["dlam"] = guarded(3, torch.float32)
     t = {n: b[1].view(q.shape if n not in ("lse", "dlam") else ((2, 2, 3, 630) if n == "lse" else (3,))) for n, b in bufs.items()}
-    ws = torch.full((max(need_f, need_b) + 256,), 7, device="cuda", dtype=torch.uint8)
+    ws = torch.full((need_b + 256,), 7, device="cuda", dtype=torch.uint8)
     ins = [x.clone() for x in (q, k, v, do, lam)]
-    sta.sta_diff_attention_fwd(q, k, v, lam, t["out"], GRID, TILE, WINDOWS, 0.18, t["out2"], t["lse"], workspace=ws[:max(need_f, 1)])
+    sta.sta_diff_attention_fwd(q, k, v, lam, t["out"], GRID, TILE, WINDOWS, 0.18, t["out2"], t["lse"])
     sta.sta_diff_attention_bwd(q, k, v, lam, t["out"], t["out2"], t["lse"], do, t["dq"], t["dk"], t["dv"], t["dlam"], GRID, TILE,
                                WINDOWS, 0.18, workspace=ws[:need_b])
     torch.cuda.synchronize()
     for n, (buf, view) in bufs.items():
         assert torch.equal(buf[view.numel():], torch.full((256,), 3.0, device="cuda", dtype=buf.dtype)), n
         assert torch.isfinite(view).all(), n
-    assert torch.equal(ws[max(need_f, need_b):], torch.full((256,), 7, device="cuda", dtype=torch.uint8))
+    assert torch.equal(ws[need_b:], torch.full((256,), 7, device="cuda", dtype=torch.uint8))
     assert same(ins, (q, k, v, do, lam))
     with pytest.raises(sta.StaError, match="SCRATCH"):
         sta.sta_diff_attention_bwd(q, k, v, lam, t["out"], t["out2"], t["lse"], do, t["dq"], t["dk"], t["dv"], t["dlam"], GRID,
