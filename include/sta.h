@@ -335,7 +335,8 @@ sta_status sta_attention_fwd_noalloc(const void* q, const void* k, const void* v
  *   tile: th * tw divides 128 and tt is a multiple of 128 / (th * tw);
  *   window_per_head: host array of `heads` entries, heads <= 256.
  * The first library call on a device allocates the status word; make it before
- * any stream capture.  batch = 0 or heads = 0 is a no-op.
+ * any stream capture, and replay no graph that holds these calls after
+ * sta_shutdown, which frees it.  batch = 0 or heads = 0 is a no-op.
  * Errors: NULL, ALIGN, ALIAS (an output overlaps another buffer), SHAPE, WINDOW,
  * HEADDIM, ARG, ARCH, CUDA.
  */

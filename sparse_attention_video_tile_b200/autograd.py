@@ -94,6 +94,8 @@ class STADiffAttentionFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, lam, grid, tile, windows, scale, token_major):
         q, k, v, lam = (x.contiguous() for x in (q, k, v, lam))
+        if not any(ctx.needs_input_grad):
+            return sta_diff_forward(q, k, v, lam, grid, tile, windows, scale, token_major)
         out, out2, lse = sta_diff_forward(q, k, v, lam, grid, tile, windows, scale, token_major, save=True)
         ctx.save_for_backward(q, k, v, lam, out, out2, lse)
         ctx.sta_args = (grid, tile, windows, scale, token_major)
@@ -154,14 +156,18 @@ class STADropoutFunction(torch.autograd.Function):
         return sta_dropout_forward(dy.contiguous(), ctx.dropout_p, rng), None, None
 
 
+def _need_rng(dropout_p, rng):
+    if dropout_p > 0 and rng is None:
+        raise ValueError("dropout needs rng, an int64 CUDA tensor [seed, offset]")
+
+
 def sta_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, dropout_p: float = 0.0, rng=None):
     """Layer norm over the last dimension of h = residual + dropout(x), with gradients:
     CUDA tensors in bf16, fp16 or fp32, weight and bias in the same type or fp32.
     Returns y, or (y, h) when there is a residual or dropout (h is the residual stream;
     its gradient flows back through the same kernel).  ``rng``: int64 CUDA tensor
     [seed, offset]; give each call of a step its own offset."""
-    if dropout_p > 0 and rng is None:
-        raise ValueError("dropout needs rng, an int64 CUDA tensor [seed, offset]")
+    _need_rng(dropout_p, rng)
     return STALayerNormFunction.apply(x, weight, bias, float(eps), residual, float(dropout_p), rng)
 
 
@@ -171,6 +177,7 @@ def sta_dropout(x, dropout_p: float, rng):
     evaluated again in the backward."""
     if dropout_p == 0:
         return x
+    _need_rng(dropout_p, rng)
     return STADropoutFunction.apply(x, float(dropout_p), rng)
 
 
@@ -190,6 +197,7 @@ def sta_diff_attention(q, k, v, lam, grid, tile, window_per_head: Sequence, scal
     ``sta_dropout`` with ``rng``."""
     if scale is None:
         scale = 1.0 / float(q.shape[-1] // 2) ** 0.5
+    _need_rng(dropout_p, rng)
     out = STADiffAttentionFunction.apply(q, k, v, lam, tuple(grid), tuple(tile), [tuple(w) for w in window_per_head],
                                          float(scale), bool(token_major))
     if norm_weight is not None or norm_bias is not None:

@@ -189,11 +189,15 @@ sta_status cuda_fail(cudaError_t e) {
 }
 
 sta_status status_word(int dev, int32_t** word) {
-  std::lock_guard<std::mutex> lock(g_mu);
-  DeviceState* st = nullptr;
-  const sta_status s = device_state(dev, &st);
-  if (s == STA_OK) *word = st->d_err;
-  return s;
+  try {   // the map may allocate; no exception leaves a C entry point
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* st = nullptr;
+    const sta_status s = device_state(dev, &st);
+    if (s == STA_OK) *word = st->d_err;
+    return s;
+  } catch (...) {
+    return STA_ERR_CUDA;
+  }
 }
 
 }  // namespace sta

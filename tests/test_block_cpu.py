@@ -195,6 +195,9 @@ def test_norm_binding_checks(lib):
     from sparse_attention_video_tile_b200 import autograd as A
     with pytest.raises(ValueError, match="rng"):
         A.sta_layer_norm(x, dropout_p=0.5)
+    with pytest.raises(ValueError, match="rng"):
+        A.sta_dropout(x, 0.5, None)
+    assert A.sta_dropout(x, 0.0, None) is x
 
 
 def test_package_imports_without_the_block_module():

@@ -112,6 +112,16 @@ def test_strided_and_half_precision_gradients_reach_the_leaves():
     assert torch.equal(out, saved[0]) and torch.equal(g, backward(q, k, v, lam, saved, do)[0])
 
 
+def test_without_gradients_nothing_is_saved():
+    q, k, v, _, lam = inputs(2)
+    want = sta.sta_diff_forward(q, k, v, lam, GRID, TILE, WINDOWS, 0.18)
+    assert torch.equal(A.sta_diff_attention(q, k, v, lam, GRID, TILE, WINDOWS, 0.18), want)
+    with torch.no_grad():
+        q.requires_grad_(True)
+        out = A.sta_diff_attention(q, k, v, lam, GRID, TILE, WINDOWS, 0.18)
+    assert torch.equal(out, want) and not out.requires_grad
+
+
 def test_second_derivative_raises():
     q, k, v, do, lam = inputs(2)
     q.requires_grad_(True)
