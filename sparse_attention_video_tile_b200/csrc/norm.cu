@@ -8,6 +8,11 @@
 // row stays in registers between its load and its store, so the variance is the sum
 // of squared differences from the mean, with no cancellation and no second read; all
 // sums are fp32.  y is taken from the fp32 h, before h is rounded for its store.
+//
+// Measured (a plain copy moves 6400 GB/s): 1 382 400 x 128 bf16 in 116 us, 6100 GB/s; 57 600 x
+// 1536 bf16 with residual and dropout in 115 us, 6150 GB/s; fp32 5000 to 5900 GB/s, from 2048
+// columns on 4100 to 5900.  Rows of an odd width are bound by the shared-memory accesses of their
+// single elements: 72 754 x 1153 bf16 1290 GB/s, 346 636 x 121 fp32 5160 GB/s.
 #include "norm_common.cuh"
 
 namespace sta {
@@ -22,7 +27,6 @@ using namespace norm;
 template <typename T, int TPR, int CH, int R, int STAGES>
 __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const NormFwdArgs a) {
   constexpr bool kBlock = TPR == 0;
-  constexpr bool kKeep = CH <= 2 && !kBlock;      // weight and bias stay in registers
   constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
   constexpr int kRows = kGroups * R;              // rows of a step
   __shared__ float red[2][R][32];   // block mode: sums of a row, of its values and of its squares
@@ -44,21 +48,19 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
   const float inv_n = 1.0f / static_cast<float>(a.cols);
   const uint32_t one = span_bytes<T>(static_cast<uint32_t>(kRows) * a.cols), stage = res != nullptr ? 2 * one : one;
   uint8_t* mine = bufs + (kBlock ? 0 : (threadIdx.x >> 5) * STAGES * stage);
-  uint64_t w[kKeep ? CH : 1][4], b[kKeep ? CH : 1][4];
-  if constexpr (kKeep) {
+  uint64_t w[CH][4], b[CH][4];   // they stay in registers
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int32_t ch = lane + k * step;
+  for (int k = 0; k < CH; ++k) {
+    const int32_t ch = lane + k * step;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[k][i] = both(1.f);
-        b[k][i] = 0;
-      }
-      if (ch < n8) {
-        const int n = min(8, a.cols - ch * 8);
-        if (a.weight != nullptr) load_param2<T>(a.weight, a.wfp32, ch * 8, n, w[k]);
-        if (a.bias != nullptr) load_param2<T>(a.bias, a.wfp32, ch * 8, n, b[k]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      w[k][i] = both(1.f);
+      b[k][i] = 0;
+    }
+    if (ch < n8) {
+      const int n = min(8, a.cols - ch * 8);
+      if (a.weight != nullptr) load_param2<T>(a.weight, a.wfp32, ch * 8, n, w[k]);
+      if (a.bias != nullptr) load_param2<T>(a.bias, a.wfp32, ch * 8, n, b[k]);
     }
   }
   auto rows_at = [&](int64_t base) { return static_cast<int>(min(static_cast<int64_t>(kRows), a.rows - base)); };
@@ -157,16 +159,6 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
         const int32_t ch = lane + k * step;
         if (ch >= n8) continue;
         const int n = min(8, a.cols - ch * 8);
-        uint64_t wk[4], bk[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          wk[i] = kKeep ? w[kKeep ? k : 0][i] : both(1.f);
-          bk[i] = kKeep ? b[kKeep ? k : 0][i] : 0;
-        }
-        if (!kKeep && out == 1) {
-          if (a.weight != nullptr) load_param2<T>(a.weight, a.wfp32, ch * 8, n, wk);
-          if (a.bias != nullptr) load_param2<T>(a.bias, a.wfp32, ch * 8, n, bk);
-        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const int q = r * kGroups + grp;
@@ -175,7 +167,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
           const uint64_t nm = both(-mean[r]), rs = both(rstd[r]);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            v[i] = out == 0 ? f[r][k][i] : fma_f32x2(mul_f32x2(add_f32x2(f[r][k][i], nm), rs), wk[i], bk[i]);
+            v[i] = out == 0 ? f[r][k][i] : fma_f32x2(mul_f32x2(add_f32x2(f[r][k][i], nm), rs), w[k][i], b[k][i]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float u, t;
@@ -206,9 +198,8 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
 // that advance by one constant, half the instructions.
 // DROP: with dropout, whose generator takes registers that the other calls use for more warps.
 template <typename T, bool DROP, int TPR, int CH, int R, int STAGES>
-__global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 ? 2 : 1) norm_fwd_vec_kernel(const NormFwdArgs a) {
+__global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 && CH <= 2 ? 2 : 1) norm_fwd_vec_kernel(const NormFwdArgs a) {
   constexpr bool kBlock = TPR == 0;
-  constexpr bool kKeep = CH <= 2 && !kBlock;      // weight and bias stay in registers
   constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
   constexpr int kRows = kGroups * R;              // rows of a step
   constexpr int kParts = Own<T>::kParts;
@@ -232,20 +223,18 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 ? 2 : 1) norm_fwd
   const int psize = a.wfp32 ? 4 : static_cast<int>(sizeof(T)), p_bytes = step * 8 * psize;
   const char* wp = static_cast<const char*>(a.weight) + lane * 8 * psize;   // this thread's first parameters
   const char* bp = static_cast<const char*>(a.bias) + lane * 8 * psize;
-  uint64_t w[kKeep ? CH : 1][4], b[kKeep ? CH : 1][4];
-  if constexpr (kKeep) {
+  uint64_t w[CH][4], b[CH][4];   // they stay in registers
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int32_t ch = lane + k * step;
+  for (int k = 0; k < CH; ++k) {
+    const int32_t ch = lane + k * step;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[k][i] = both(1.f);
-        b[k][i] = 0;
-      }
-      if (ch < n8) {
-        if (a.weight != nullptr) read_param2<T>(wp + k * p_bytes, a.wfp32, w[k]);
-        if (a.bias != nullptr) read_param2<T>(bp + k * p_bytes, a.wfp32, b[k]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      w[k][i] = both(1.f);
+      b[k][i] = 0;
+    }
+    if (ch < n8) {
+      if (a.weight != nullptr) read_param2<T>(wp + k * p_bytes, a.wfp32, w[k]);
+      if (a.bias != nullptr) read_param2<T>(bp + k * p_bytes, a.wfp32, b[k]);
     }
   }
   // Addresses: one pointer per array, at this thread's first chunk of a step's first row; a
@@ -340,22 +329,12 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 ? 2 : 1) norm_fwd
     for (int k = 0; k < CH; ++k) {
       const int32_t ch = lane + k * step;
       if (ch >= n8) continue;
-      uint64_t wk[4], bk[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        wk[i] = kKeep ? w[kKeep ? k : 0][i] : both(1.f);
-        bk[i] = kKeep ? b[kKeep ? k : 0][i] : 0;
-      }
-      if (!kKeep) {
-        if (a.weight != nullptr) read_param2<T>(wp + k * p_bytes, a.wfp32, wk);
-        if (a.bias != nullptr) read_param2<T>(bp + k * p_bytes, a.wfp32, bk);
-      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const uint64_t rs = both(rstd[r]);
         uint64_t v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = fma_f32x2(mul_f32x2(f[r][k][i], rs), wk[i], bk[i]);
+        for (int i = 0; i < 4; ++i) v[i] = fma_f32x2(mul_f32x2(f[r][k][i], rs), w[k][i], b[k][i]);
         if (r * kGroups < left) Own<T>::write(py + r * r_bytes + k * k_bytes, v);
       }
     }
@@ -403,25 +382,46 @@ cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// A warp takes rows of up to 1536 columns (48 values of a row in a thread's registers), a
-// block longer ones.  Short rows: two chunks a thread rather than one, which halves the
-// shuffles of a row's sums.
+// A warp takes rows of up to 1536 columns (48 values of a row, weight and bias in a thread's
+// registers), a block longer ones.  Stages and rows of a step by what was fastest; the rates
+// are of plain calls over 170 M elements, bf16 and fp32, in GB/s:
+//   128 columns: 16 threads a row 6140, 8 threads (half the shuffles, fewer rows in flight) 5150;
+//   512: one row a step and three stages 6160 and 5320, two rows and four (two) 5140 and 5310;
+//   1024: a warp and two rows (fp32: one) 6180 and 5620, a block a row 4970 and 5260;
+//   1536: a warp 6090 and 5210, a block 4480 and 4430;
+//   weight and bias read again for every row: 4580 and 5040 at 1024 columns, 4530 and 4430 at 1536;
+//   2048 and more: two rows a step 5520 and 5910, one 3840 and 4440 (4096: 5370 and 5440, 3600 and
+//   4030).  Above 4096 columns two fp32 rows with a residual do not fit in shared memory.
+// Rows that go through spans keep fewer threads a row up to 512 columns: there the reads from
+// shared memory bind, and 8 threads a row move 2880 and 5190 at 121 columns, 16 2290 and 3770.
 template <typename T, bool VEC>
 cudaError_t pick_fwd(const NormFwdArgs& a, cudaStream_t stream) {
-  constexpr int S = sizeof(T) == 4 ? 2 : 4;   // 4 KB a stage, array and warp at most
+  constexpr bool k16 = sizeof(T) == 2;
   const int n8 = (a.cols + 7) >> 3;
-  if (n8 <= 1) return launch_fwd<T, VEC, 1, 1, 2, S>(a, stream);
-  if (n8 <= 4) return launch_fwd<T, VEC, 2, 2, 2, S>(a, stream);
-  if (n8 <= 8) return launch_fwd<T, VEC, 4, 2, 2, S>(a, stream);
-  if (n8 <= 16) return launch_fwd<T, VEC, 8, 2, 2, S>(a, stream);
-  if (n8 <= 32) return launch_fwd<T, VEC, 16, 2, 2, S>(a, stream);
-  if (n8 <= 64) return launch_fwd<T, VEC, 32, 2, 2, S>(a, stream);
-  if (n8 <= 128) return launch_fwd<T, VEC, 32, 4, 1, 2>(a, stream);
-  if (n8 <= 192 && sizeof(T) == 2) return launch_fwd<T, VEC, 32, 6, 1, 2>(a, stream);
+  if (n8 <= 1) return launch_fwd<T, VEC, 1, 1, 2, k16 ? 4 : 2>(a, stream);
+  if constexpr (VEC) {
+    if (n8 <= 4) return launch_fwd<T, VEC, 4, 1, 2, 3>(a, stream);
+    if (n8 <= 8) return launch_fwd<T, VEC, 8, 1, k16 ? 2 : 4, 3>(a, stream);
+    if (n8 <= 16) return launch_fwd<T, VEC, 16, 1, k16 ? 4 : 2, k16 ? 2 : 3>(a, stream);
+    if (n8 <= 32) return launch_fwd<T, VEC, k16 ? 16 : 32, k16 ? 2 : 1, k16 ? 1 : 2, 3>(a, stream);
+    if (n8 <= 64) return launch_fwd<T, VEC, 32, 2, 1, 3>(a, stream);
+  } else {
+    constexpr int S = k16 ? 4 : 2;
+    if (n8 <= 4) return launch_fwd<T, VEC, 2, 2, 2, S>(a, stream);
+    if (n8 <= 8) return launch_fwd<T, VEC, 4, 2, 2, S>(a, stream);
+    if (n8 <= 16) return launch_fwd<T, VEC, 8, 2, 2, S>(a, stream);
+    if (n8 <= 32) return launch_fwd<T, VEC, 16, 2, 2, S>(a, stream);
+    if (n8 <= 64) return launch_fwd<T, VEC, 32, 2, 2, S>(a, stream);
+  }
+  if (n8 <= 128) return launch_fwd<T, VEC, 32, 4, k16 ? 2 : 1, 2>(a, stream);
+  if (n8 <= 192) return launch_fwd<T, VEC, 32, 6, 1, k16 ? 3 : 2>(a, stream);
+  if (k16 || n8 <= 512) return launch_fwd<T, VEC, 0, 2, 2, 2>(a, stream);
   return launch_fwd<T, VEC, 0, 2, 1, 2>(a, stream);
 }
 
 // Dropout, rows of a multiple of eight columns: chunk i of the flat array is counter block i.
+// Four chunks a thread, all loaded first: 115 200 x 1536 bf16 in 119 us, 5950 GB/s (a copy takes
+// 111 us); two chunks 134 us, eight 120 us.
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_kernel(const T* __restrict__ x, T* __restrict__ y, int64_t chunks,
                                                       const NormDropout drop) {
@@ -451,7 +451,9 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T* __restrict__ x, T
 
 // Dropout, any number of columns: a thread takes eight consecutive elements of the
 // flat array (16-byte aligned), which lie in one or more rows, and evaluates every
-// counter block that they touch (two in most places).
+// counter block that they touch (two in most places).  Bound by the generator, which runs twice
+// per chunk: 3290 GB/s for rows that the kernel above takes at 5950; 80 M elements in rows of 1153
+// bf16 2120 GB/s, fp32 3760.
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_any_kernel(const T* __restrict__ x, T* __restrict__ y, int64_t total,
                                                           int32_t cols, const NormDropout drop) {

@@ -9,6 +9,11 @@
 // part once, and a second kernel adds the parts in a fixed order, so the weight's
 // gradient is the same in every run.  The dropout mask is evaluated again from the
 // generator.
+//
+// Measured (a plain copy moves 6400 GB/s): 1 382 400 x 128 bf16 in 174 us, 6100 GB/s; 57 600 x
+// 1536 bf16 with the gradient that reaches h, dropout and both outputs in 180 us, 4900 GB/s, bound
+// by the generator's and the row's instructions at 16 warps an SM; fp32 4500 to 5900 GB/s; odd
+// widths 1200 to 4200 GB/s, bound by the shared-memory accesses of their single elements.
 #include "norm_common.cuh"
 
 namespace sta {
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
 // The same for rows of a multiple of eight columns (see Own).
 // DROP: with dropout, whose generator takes registers that the other calls use for more warps.
 template <typename T, bool DROP, int TPR, int CH, int R, int STAGES>
-__global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 ? 2 : 1) norm_bwd_vec_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(TPR > 0 ? 256 : CH * R == 4 ? 384 : 512, TPR > 0 && CH <= 2 ? 2 : 1) norm_bwd_vec_kernel(const NormBwdArgs a) {
   constexpr bool kBlock = TPR == 0;
   constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
   constexpr int kRows = kGroups * R;   // rows of a warp's (block's) step
@@ -477,29 +482,51 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
   }
 }
 
-// Launch shape of the first kernel: threads that share a row (0: the block), threads of a
-// block, blocks.  It depends on the sizes alone, and so do the parts and the sums' order.
+// Launch shape of the first kernel: threads that share a row (0: the block), chunks of a
+// thread, rows of a block's step, threads of a block, blocks.  It depends on the sizes and the
+// type alone, and so do the parts and the sums' order.  No more blocks than an SM holds (128
+// registers a thread, 168 where a thread has two chunks of two rows).  Rates of plain calls over
+// 170 M elements and of calls with every option over 85 M, in GB/s:
+//   1024 columns: a warp a row, one block an SM: bf16 6000 and 5880, fp32 5700 and 4930; a block a
+//   row: 5390 and 4800, 5980 and 4510;
+//   bf16 blocks: two chunks and two rows 6100 and 4870 at 1536 columns, 5160 and 4590 at 4096; one
+//   chunk and two rows 5220 and 4870, 5210 and 4750;
+//   fp32 blocks: one chunk and two rows 6230 and 5490 at 1536 columns, 5230 and 4650 at 4096; two
+//   chunks of one row 5440 and 5740, 5860 and 5430; two and two 4090 and 3540 at 1536;
+//   above 4096 columns: one block an SM 4570 and fp32 5690 at 5120 columns, two 4380 and 5440.
 struct BwdShape {
-  int tpr, threads;
+  int tpr, ch, rows, threads;
   int64_t blocks;
 };
 
-BwdShape bwd_shape(int64_t rows, int32_t cols) {
+BwdShape bwd_shape(int64_t rows, int32_t cols, bool fp32) {
   const int n8 = (cols + 7) >> 3;
+  const bool vec = (cols & 7) == 0;
   BwdShape s{};
-  s.tpr = n8 <= 1 ? 1 : n8 <= 4 ? 2 : n8 <= 8 ? 4 : n8 <= 16 ? 8 : n8 <= 32 ? 16 : n8 <= 64 ? 32 : 0;
+  s.tpr = n8 <= 1 ? 1 : n8 <= 4 ? 2 : n8 <= 8 ? 4 : n8 <= 16 ? 8 : n8 <= 32 ? 16 : n8 <= (vec ? 128 : 64) ? 32 : 0;
   int per_sm;
   int64_t block_rows;
   if (s.tpr > 0) {
+    s.ch = n8 <= 1 ? 1 : n8 <= 64 ? 2 : 4;
+    s.rows = 1;
     s.threads = 256;
     block_rows = static_cast<int64_t>(256 / s.tpr);
-    per_sm = 2;
+    per_sm = s.ch <= 2 ? 2 : 1;
   } else {
-    const int ch = n8 <= 512 ? 1 : 2;
-    s.threads = ((n8 + ch - 1) / ch + 31) / 32 * 32;
-    block_rows = ch == 1 ? 2 : 1;
-    per_sm = (ch == 1 ? 1024 : 640) / s.threads;
-    per_sm = per_sm < 1 ? 1 : per_sm;
+    if (n8 > 512) {
+      s.ch = 2;
+      s.rows = 1;
+    } else if (!vec) {
+      s.ch = 1;
+      s.rows = cols * (fp32 ? 4 : 2) <= 8192 ? 4 : 2;   // see bwd_t
+    } else {
+      s.ch = fp32 && n8 <= 256 ? 1 : 2;
+      s.rows = fp32 && n8 > 256 ? 1 : 2;
+    }
+    s.threads = ((n8 + s.ch - 1) / s.ch + 31) / 32 * 32;
+    block_rows = s.rows;
+    per_sm = n8 > 512 ? 1 : (s.ch * s.rows == 4 && vec ? 384 : 512) / s.threads;
+    if (per_sm < 1) per_sm = 1;
   }
   const int64_t need = (rows + block_rows - 1) / block_rows;
   s.blocks = need < 148 * per_sm ? need : 148 * per_sm;
@@ -527,18 +554,37 @@ cudaError_t launch_bwd(const NormBwdArgs& a, const BwdShape& s, cudaStream_t str
 
 template <typename T, bool VEC>
 cudaError_t bwd_t(const NormBwdArgs& a, cudaStream_t stream) {
-  const BwdShape s = bwd_shape(a.rows, a.cols);
+  const BwdShape s = bwd_shape(a.rows, a.cols, sizeof(T) == 4);
   if (a.rows > 0) {
     cudaError_t e;
     switch (s.tpr) {
       case 1: e = launch_bwd<T, VEC, 1, 1, 1, 4>(a, s, stream); break;
       case 2: e = launch_bwd<T, VEC, 2, 2, 1, 4>(a, s, stream); break;
       case 4: e = launch_bwd<T, VEC, 4, 2, 1, 4>(a, s, stream); break;
-      case 8: e = launch_bwd<T, VEC, 8, 2, 1, 4>(a, s, stream); break;
+      // three stages: 6080 and 5130 plain, 5290 and 5910 with every option; four: 5900 and 5870, 5020 and 4450
+      case 8: e = launch_bwd<T, VEC, 8, 2, 1, 3>(a, s, stream); break;
       case 16: e = launch_bwd<T, VEC, 16, 2, 1, 4>(a, s, stream); break;
-      case 32: e = launch_bwd<T, VEC, 32, 2, 1, 4>(a, s, stream); break;
+      case 32:
+        if constexpr (VEC) {
+          if (s.ch == 4) {
+            e = launch_bwd<T, VEC, 32, 4, 1, 2>(a, s, stream);
+            break;
+          }
+        }
+        e = launch_bwd<T, VEC, 32, 2, 1, 4>(a, s, stream);
+        break;
       default:
-        e = a.cols <= 4096 ? launch_bwd<T, VEC, 0, 1, 2, 2>(a, s, stream) : launch_bwd<T, VEC, 0, 2, 1, 2>(a, s, stream);
+        if (s.ch == 2 && s.rows == 1) {
+          e = launch_bwd<T, VEC, 0, 2, 1, 2>(a, s, stream);
+        } else if constexpr (!VEC) {
+          // through spans a step costs five barriers: four rows share them where they fit in shared
+          // memory (1153 columns: 1840 GB/s, fp32 2490; two rows 1550 and 1970)
+          e = s.rows == 4 ? launch_bwd<T, VEC, 0, 1, 4, 2>(a, s, stream) : launch_bwd<T, VEC, 0, 1, 2, 2>(a, s, stream);
+        } else if constexpr (sizeof(T) == 4) {
+          e = launch_bwd<T, VEC, 0, 1, 2, 2>(a, s, stream);
+        } else {
+          e = launch_bwd<T, VEC, 0, 2, 2, 2>(a, s, stream);
+        }
     }
     if (e != cudaSuccess) return e;
   }
@@ -552,7 +598,10 @@ cudaError_t bwd_t(const NormBwdArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-int norm_bwd_parts(int64_t rows, int32_t cols) { return static_cast<int>(bwd_shape(rows, cols).blocks); }
+int norm_bwd_parts(int64_t rows, int32_t cols) {
+  const int64_t a = bwd_shape(rows, cols, false).blocks, b = bwd_shape(rows, cols, true).blocks;
+  return static_cast<int>(a > b ? a : b);
+}
 
 cudaError_t launch_norm_bwd(int dtype, const NormBwdArgs& a, cudaStream_t stream) {
   const bool vec = (a.cols & 7) == 0;
