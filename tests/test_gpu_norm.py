@@ -173,17 +173,16 @@ def test_dropped_values_leave_zeros():
 
 
 def test_counter_passes_32_bits():
-    """Rows far down a tall array: the counter's high word is used."""
-    rows, cols = 3 * 2 ** 28 + 5, 1      # one block per row and 805 million rows
-    # 2^32 blocks would need more memory than the check is worth; the 64-bit product is checked
-    # on a row range whose flat element number passes 2^31 in bytes
-    x = torch.ones(rows, cols, device="cuda", dtype=torch.bfloat16)
+    """More than 2^32 counter blocks, one per row: the counter's high word is used."""
+    rows = 2 ** 32 + 5
+    x = torch.ones(rows, 1, device="cuda", dtype=torch.bfloat16)
     y = sta.sta_dropout_forward(x, 0.5, torch.tensor([11, 22], device="cuda"))
-    tail = y[-8:].float().cpu().numpy()
-    for i in range(8):
-        n = rows - 8 + i
-        w = B.philox((n & 0xFFFFFFFF, n >> 32, 22, 0), (11, 0))
-        assert tail[i, 0] == (2.0 if (w[0] & 0xFFFF) >= 32768 else 0.0)
+    for first in (2 ** 31 - 4, rows - 12):
+        got = y[first:first + 12].float().cpu().numpy()
+        for i in range(12):
+            n = first + i
+            w = B.philox((n & 0xFFFFFFFF, n >> 32, 22, 0), (11, 0))
+            assert got[i, 0] == (2.0 if (w[0] & 0xFFFF) >= 32768 else 0.0), n
 
 
 def test_rows_and_columns_past_the_array_stay():
