@@ -11,8 +11,9 @@
 //
 // Measured (a plain copy moves 6400 GB/s): 1 382 400 x 128 bf16 in 116 us, 6100 GB/s; 57 600 x
 // 1536 bf16 with residual and dropout in 115 us, 6150 GB/s; fp32 5000 to 5900 GB/s, from 2048
-// columns on 4100 to 5900.  Rows of an odd width are bound by the shared-memory accesses of their
-// single elements: 72 754 x 1153 bf16 1290 GB/s, 346 636 x 121 fp32 5160 GB/s.
+// columns on 4100 to 5900.  Rows of an odd width pass shared memory four times and are bound by
+// that, their shifts and their barriers: 36 377 x 1153 bf16 2000 GB/s, fp32 3290; 173 318 x 121 fp32
+// 4360; 2 M x 20 bf16 2160.
 #include "norm_common.cuh"
 
 namespace sta {
@@ -29,6 +30,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
   constexpr bool kBlock = TPR == 0;
   constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
   constexpr int kRows = kGroups * R;              // rows of a step
+  constexpr bool kOwnRows = kBlock || CH > 2;    // how a row goes out
   __shared__ float red[2][R][32];   // block mode: sums of a row, of its values and of its squares
   extern __shared__ __align__(16) uint8_t bufs[];
   const int lane = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x & 31) % (TPR > 0 ? TPR : 1);
@@ -46,7 +48,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
   PhiloxKey key{};
   if (a.drop.thr > 0) key = philox_key(a.drop.rng);
   const float inv_n = 1.0f / static_cast<float>(a.cols);
-  const uint32_t one = span_bytes<T>(static_cast<uint32_t>(kRows) * a.cols), stage = res != nullptr ? 2 * one : one;
+  const uint32_t one = span_stage<T>(kRows, a.cols), stage = res != nullptr ? 2 * one : one;
   uint8_t* mine = bufs + (kBlock ? 0 : (threadIdx.x >> 5) * STAGES * stage);
   uint64_t w[CH][4], b[CH][4];   // they stay in registers
 #pragma unroll
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int q = r * kGroups + grp, c0 = (lane + k * step) * 8;
-        span_get<T>(ex, q * a.cols + c0, q < live ? a.cols - c0 : 0, f[r][k]);
+        span_get<T, TPR == 1>(ex, q * a.cols + c0, q < live ? a.cols - c0 : 0, f[r][k]);
       }
     if (a.drop.thr > 0) {
 #pragma unroll
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
         for (int k = 0; k < CH; ++k) {
           const int q = r * kGroups + grp, c0 = (lane + k * step) * 8;
           uint64_t g[4];
-          span_get<T>(er, q * a.cols + c0, q < live ? a.cols - c0 : 0, g);
+          span_get<T, TPR == 1>(er, q * a.cols + c0, q < live ? a.cols - c0 : 0, g);
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[r][k][i] = add_f32x2(f[r][k][i], g[i]);
         }
@@ -153,7 +155,9 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
       T* dst = out == 0 ? h : y;
       if (dst == nullptr) continue;
       span_sync<kBlock>();   // the slot's values are in registers (or stored): it carries the output
+      // long rows lie on boundaries of their own (row_put), shorter ones as the span
       T* eo = span_elems(p, dst + base * a.cols);
+      const uint32_t pitch = static_cast<uint32_t>(n8) * 8 * sizeof(T);
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int32_t ch = lane + k * step;
@@ -168,17 +172,29 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             v[i] = out == 0 ? f[r][k][i] : fma_f32x2(mul_f32x2(add_f32x2(f[r][k][i], nm), rs), w[k][i], b[k][i]);
+          if constexpr (kOwnRows) {
+            row_put<T>(static_cast<uint32_t>(__cvta_generic_to_shared(p)) + q * pitch + ch * 8 * sizeof(T), v);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float u, t;
-            f32x2_split(v[i], u, t);
-            if (2 * i < n) eo[q * a.cols + ch * 8 + 2 * i] = from_f<T>(u);
-            if (2 * i + 1 < n) eo[q * a.cols + ch * 8 + 2 * i + 1] = from_f<T>(t);
+            for (int i = 0; i < 4; ++i) {
+              float u, t;
+              f32x2_split(v[i], u, t);
+              if (2 * i < n) eo[q * a.cols + ch * 8 + 2 * i] = from_f<T>(u);
+              if (2 * i + 1 < n) eo[q * a.cols + ch * 8 + 2 * i + 1] = from_f<T>(t);
+            }
           }
         }
       }
       span_sync<kBlock>();
-      span_store(p, dst + base * a.cols, live * a.cols, st, snt);
+      if constexpr (kOwnRows) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int q = r * kGroups + grp;
+          if (q < live) row_store(p + q * pitch, dst + (base + q) * a.cols, a.cols, lane, step);
+        }
+      } else {
+        span_store(p, dst + base * a.cols, live * a.cols, st, snt);
+      }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -367,18 +383,21 @@ cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t stream) {
   if (TPR == 0) threads = (((a.cols + 7) / 8 + CH - 1) / CH + 31) / 32 * 32;
   const int per_block = (TPR > 0 ? threads / 32 : 1);
   const int stage = VEC ? R * CH * threads * 8 * static_cast<int>(sizeof(T))
-                        : per_block * static_cast<int>(span_bytes<T>(static_cast<uint32_t>(rows) * a.cols));
-  const int smem = STAGES * (a.residual != nullptr ? 2 : 1) * stage;
+                        : per_block * static_cast<int>(span_stage<T>(rows, a.cols));
+  const int smem = STAGES * (a.residual != nullptr ? 2 : 1) * stage + (VEC ? 0 : kSpanSlack);
   int sms = 0, dev = 0, fit = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, threads, smem);
   if (e != cudaSuccess) return e;
-  if (fit < 1) return cudaErrorInvalidConfiguration;
   const int64_t need = ((a.rows + rows - 1) / rows + per_block - 1) / per_block;
-  const int64_t most = static_cast<int64_t>(sms) * fit;
-  kern<<<static_cast<unsigned>(need < most ? need : most), threads, smem, stream>>>(a);
+  int64_t blocks = need;
+  if (need > sms) {   // a persistent grid: as many blocks as the SMs hold (a small call saves the query)
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kern, threads, smem)) != cudaSuccess) return e;
+    if (fit < 1) return cudaErrorInvalidConfiguration;
+    if (blocks > static_cast<int64_t>(sms) * fit) blocks = static_cast<int64_t>(sms) * fit;
+  }
+  kern<<<static_cast<unsigned>(blocks), threads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -13,7 +13,8 @@
 // Measured (a plain copy moves 6400 GB/s): 1 382 400 x 128 bf16 in 174 us, 6100 GB/s; 57 600 x
 // 1536 bf16 with the gradient that reaches h, dropout and both outputs in 180 us, 4900 GB/s, bound
 // by the generator's and the row's instructions at 16 warps an SM; fp32 4500 to 5900 GB/s; odd
-// widths 1200 to 4200 GB/s, bound by the shared-memory accesses of their single elements.
+// widths from 9 columns on 1000 to 4000 GB/s (36 377 x 1153 bf16 2080, fp32 3210), bound by their
+// passes through shared memory and the barriers.
 #include "norm_common.cuh"
 
 namespace sta {
@@ -55,6 +56,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
   constexpr bool kBlock = TPR == 0;
   constexpr int kGroups = kBlock ? 1 : 32 / (TPR > 0 ? TPR : 1);
   constexpr int kRows = kGroups * R;   // rows of a warp's (block's) step
+  constexpr bool kOwnRows = kBlock || TPR >= 16;   // how a row goes out
   // block mode: partial row sums, a buffer per row in flight and per step parity
   __shared__ float2 red[2][R][32];
   extern __shared__ __align__(16) uint8_t bufs[];
@@ -71,7 +73,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
   const T* dh = static_cast<const T*>(a.dh);
   PhiloxKey key{};
   if (a.drop.thr > 0) key = philox_key(a.drop.rng);
-  const uint32_t one = span_bytes<T>(static_cast<uint32_t>(kRows) * a.cols), stage = (dh != nullptr ? 3 : 2) * one;
+  const uint32_t one = span_stage<T>(kRows, a.cols), stage = (dh != nullptr ? 3 : 2) * one;
   uint8_t* mine = bufs + (kBlock ? 0 : (threadIdx.x >> 5) * STAGES * stage);
   uint64_t w[CH][4], dw[CH][4], db[CH][4];   // pairs of columns
 #pragma unroll
@@ -131,8 +133,8 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int c0 = (lane + k * step) * 8, e0 = q * a.cols + c0, n = q < live ? a.cols - c0 : 0;
-        span_get<T>(ey, e0, n, g[r][k]);
-        span_get<T>(ez, e0, n, z[r][k]);
+        span_get<T, TPR == 1>(ey, e0, n, g[r][k]);
+        span_get<T, TPR == 1>(ez, e0, n, z[r][k]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint64_t y = g[r][k][i];
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
         if (dh != nullptr) {
           const int q = r * kGroups + grp, c0 = (lane + k * step) * 8;
           uint64_t d2[4];
-          span_get<T>(ed, q * a.cols + c0, q < live ? a.cols - c0 : 0, d2);
+          span_get<T, TPR == 1>(ed, q * a.cols + c0, q < live ? a.cols - c0 : 0, d2);
 #pragma unroll
           for (int i = 0; i < 4; ++i) g[r][k][i] = add_f32x2(g[r][k][i], d2[i]);
         }
@@ -174,7 +176,9 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
       T* dst = static_cast<T*>(out == 0 ? a.dres : a.dx);
       if (dst == nullptr) continue;
       span_sync<kBlock>();   // the slot's values are in registers (or stored): it carries the output
+      // long rows lie on boundaries of their own (row_put), shorter ones as the span
       T* eo = span_elems(p, dst + base * a.cols);
+      const uint32_t pitch = static_cast<uint32_t>(n8) * 8 * sizeof(T);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int q = r * kGroups + grp;
@@ -187,18 +191,30 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = g[r][k][i];
           if (out == 1 && a.drop.thr > 0) drop_pairs(v, static_cast<uint64_t>(base + q) * n8 + ch, key, a.drop);
-          const int n = min(8, a.cols - ch * 8);
+          if constexpr (kOwnRows) {
+            row_put<T>(static_cast<uint32_t>(__cvta_generic_to_shared(p)) + q * pitch + ch * 8 * sizeof(T), v);
+          } else {
+            const int n = min(8, a.cols - ch * 8);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float u, t;
-            f32x2_split(v[i], u, t);
-            if (2 * i < n) eo[q * a.cols + ch * 8 + 2 * i] = from_f<T>(u);
-            if (2 * i + 1 < n) eo[q * a.cols + ch * 8 + 2 * i + 1] = from_f<T>(t);
+            for (int i = 0; i < 4; ++i) {
+              float u, t;
+              f32x2_split(v[i], u, t);
+              if (2 * i < n) eo[q * a.cols + ch * 8 + 2 * i] = from_f<T>(u);
+              if (2 * i + 1 < n) eo[q * a.cols + ch * 8 + 2 * i + 1] = from_f<T>(t);
+            }
           }
         }
       }
       span_sync<kBlock>();
-      span_store(p, dst + base * a.cols, live * a.cols, st, snt);
+      if constexpr (kOwnRows) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int q = r * kGroups + grp;
+          if (q < live) row_store(p + q * pitch, dst + (base + q) * a.cols, a.cols, lane, step);
+        }
+      } else {
+        span_store(p, dst + base * a.cols, live * a.cols, st, snt);
+      }
     }
     span_sync<kBlock>();   // every thread is done with the slot: the next step's fetch fills it
     slot = slot + 1 == STAGES ? 0 : slot + 1;
@@ -544,8 +560,8 @@ cudaError_t launch_bwd(const NormBwdArgs& a, const BwdShape& s, cudaStream_t str
   constexpr int rows = (TPR > 0 ? 32 / (TPR > 0 ? TPR : 1) : 1) * R;
   const int units = TPR > 0 ? s.threads / 32 : 1;
   const int stage = VEC ? R * CH * s.threads * 8 * static_cast<int>(sizeof(T))
-                        : units * static_cast<int>(span_bytes<T>(static_cast<uint32_t>(rows) * a.cols));
-  const int smem = STAGES * (a.dh != nullptr ? 3 : 2) * stage;
+                        : units * static_cast<int>(span_stage<T>(rows, a.cols));
+  const int smem = STAGES * (a.dh != nullptr ? 3 : 2) * stage + (VEC ? 0 : kSpanSlack);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(s.blocks), s.threads, smem, stream>>>(a);

@@ -176,11 +176,17 @@ __device__ __forceinline__ void Chunk<T>::set(const T (&e)[8]) {
 // Consecutive rows are one span of memory.  A span is copied to shared memory ahead of its
 // use, in 16-byte asynchronous copies that need no registers, and (rows whose length is no
 // multiple of eight start anywhere) back from there: in aligned blocks, at the same offset
-// inside a block on both sides, element by element only in a block that the span does not
-// fill.  Element i of a span whose global address is g lies at buf + (g mod 16) + i size.
+// inside a block on both sides; the copy back goes element by element in a block that the
+// span does not fill.  Element i of a span whose global address is g lies at buf + (g mod 16) + i size.
 template <typename T>
 __host__ __device__ constexpr uint32_t span_bytes(uint32_t n) {
   return (n * static_cast<uint32_t>(sizeof(T)) + 15) / 16 * 16 + 16;
+}
+// A stage of one array: the span of `rows` rows, or the rows on boundaries of their own (row_put).
+template <typename T>
+__host__ __device__ constexpr uint32_t span_stage(uint32_t rows, uint32_t cols) {
+  const uint32_t a = span_bytes<T>(rows * cols), b = rows * ((cols + 7) / 8 * 8) * static_cast<uint32_t>(sizeof(T));
+  return a > b ? a : b;
 }
 template <typename T>
 __device__ __forceinline__ T* span_elems(uint8_t* buf, const T* g) {
@@ -194,12 +200,10 @@ __device__ __forceinline__ void span_load(uint8_t* buf, const T* g, int n, int t
   const uint8_t* base = reinterpret_cast<const uint8_t*>(g) - off;
   const uint32_t sbuf = static_cast<uint32_t>(__cvta_generic_to_shared(buf));
   for (uint32_t b = static_cast<uint32_t>(t) * 16; b < end; b += static_cast<uint32_t>(nt) * 16) {
-    if (b >= off && b + 16 <= end) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sbuf + b), "l"(base + b) : "memory");
-    } else {
-      const uint32_t lo = b < off ? off : b, hi = b + 16 < end ? b + 16 : end;
-      for (uint32_t x = lo; x < hi; x += sizeof(T)) *reinterpret_cast<T*>(buf + x) = *reinterpret_cast<const T*>(base + x);
-    }
+    // what lies before the span in its first block belongs to the same array, whose start is aligned;
+    // nothing is read behind the span
+    const uint32_t size = end - b < 16u ? end - b : 16u;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sbuf + b), "l"(base + b), "r"(size) : "memory");
   }
 }
 __device__ __forceinline__ void span_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -221,12 +225,89 @@ __device__ __forceinline__ void span_store(const uint8_t* buf, T* g, int n, int 
     }
   }
 }
-// Eight elements of a span from e0 on, as pairs of fp32; those from n on read as zero.
-template <typename T>
-__device__ __forceinline__ void span_get(const T* e, int e0, int n, uint64_t (&f)[4]) {
+// 16 bytes of shared memory, at an address of a multiple of 16.
+__device__ __forceinline__ uint4 smem_read16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
+__device__ __forceinline__ void smem_write16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// N words from shared address `at`, a multiple of the element size (2 or 4): whole 16-byte blocks
+// are read, and the words moved into place in registers.  Element by element the accesses
+// conflict four ways (16 bytes a lane) or eight (32): forward at 4001 columns bf16 2350 GB/s
+// this way and 2010 that way, backward at 257 fp32 2260 and 2030.  Reads up to 16 bytes past the
+// last word's block.
+template <int N, bool HALVES>
+__device__ __forceinline__ void smem_words(uint32_t at, uint32_t (&o)[N]) {
+  const uint32_t off = at & 15u;
+  uint32_t w[N + 4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f[i] = f32x2(2 * i < n ? to_f<T>(e[e0 + 2 * i]) : 0.f, 2 * i + 1 < n ? to_f<T>(e[e0 + 2 * i + 1]) : 0.f);
+  for (int i = 0; i < N / 4 + 1; ++i) {
+    const uint4 v = smem_read16(at - off + 16 * i);
+    w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+  }
+#pragma unroll
+  for (int i = 0; i < N + 2; ++i) w[i] = off & 8u ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < N + 1; ++i) w[i] = off & 4u ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = HALVES ? __funnelshift_r(w[i], w[i + 1], (off & 2u) * 8) : w[i];
+}
+// Bytes of shared memory that such reads may touch past the last stage.
+constexpr int kSpanSlack = 64;
+// Eight elements of a span from e0 on, as pairs of fp32; those from n on read as zero.  Rows of
+// less than eight columns are read by elements, 8 % faster there.
+template <typename T, bool SHORT>
+__device__ __forceinline__ void span_get(const T* e, int e0, int n, uint64_t (&f)[4]) {
+  if constexpr (SHORT) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = f32x2(2 * i < n ? to_f<T>(e[e0 + 2 * i]) : 0.f, 2 * i + 1 < n ? to_f<T>(e[e0 + 2 * i + 1]) : 0.f);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = 0;
+  if (n <= 0) return;
+  Chunk<T> c;
+  smem_words<Chunk<T>::kWords, sizeof(T) == 2>(static_cast<uint32_t>(__cvta_generic_to_shared(e + e0)), c.w);
+  c.get2(f);
+  if (n >= 8) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float u, v;
+    f32x2_split(f[i], u, v);
+    f[i] = f32x2(2 * i < n ? u : 0.f, 2 * i + 1 < n ? v : 0.f);
+  }
+}
+// Output rows: each lies on a 16-byte boundary of shared memory (pitch n8 chunks), its chunks
+// written whole, and goes out in the 16-byte blocks of its place in memory, element by
+// element only at its two ends.  Long rows only: forward at 1153 columns 2000 GB/s (as a span
+// 1710; fp32 3300 and 2520), at 121 2630 (2820; fp32 2730 and 4390); backward at 257 columns 1390
+// (1260; fp32 2440 and 2260), at 57 2120 (2400; fp32 2270 and 2670).
+template <typename T>
+__device__ __forceinline__ void row_put(uint32_t at, const uint64_t (&f)[4]) {
+  Chunk<T> c;
+  c.put2(f);
+#pragma unroll
+  for (int i = 0; i < Chunk<T>::kWords / 4; ++i) smem_write16(at + 16 * i, c.w[4 * i], c.w[4 * i + 1], c.w[4 * i + 2], c.w[4 * i + 3]);
+}
+template <typename T>
+__device__ __forceinline__ void row_store(const uint8_t* buf, T* g, int cols, int t, int nt) {
+  constexpr int kSize = static_cast<int>(sizeof(T));
+  const int bytes = cols * kSize;
+  const int head = min((16 - static_cast<int>(reinterpret_cast<uintptr_t>(g) & 15u)) & 15, bytes), full = (bytes - head) >> 4;
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(buf)) + head;
+  uint8_t* base = reinterpret_cast<uint8_t*>(g) + head;
+  for (int j = t; j < full; j += nt) {
+    uint32_t o[4];
+    smem_words<4, sizeof(T) == 2>(at + 16 * j, o);
+    *reinterpret_cast<uint4*>(base + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  const T* e = reinterpret_cast<const T*>(buf);
+  for (int x = t; x < head / kSize; x += nt) g[x] = e[x];
+  for (int x = (head + 16 * full) / kSize + t; x < cols; x += nt) g[x] = e[x];
 }
 // Pairs through the dropout mask.  Dropped values are replaced, not multiplied by zero: an
 // infinity or NaN there stays out.
@@ -255,11 +336,6 @@ __device__ __forceinline__ void own_copy_or_zero(uint32_t dst, const void* src, 
   else
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
 }
-__device__ __forceinline__ uint4 own_read(uint32_t src) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
-  return v;
-}
 // A chunk is kParts 16-byte parts; part p of chunk i of a stage lies at (i kParts + p) 16 threads + 16 thread.
 template <typename T>
 struct Own {
@@ -272,7 +348,7 @@ struct Own {
     Chunk<T> c;
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
-      const uint4 v = own_read(at + p * part);
+      const uint4 v = smem_read16(at + p * part);
       c.w[4 * p] = v.x; c.w[4 * p + 1] = v.y; c.w[4 * p + 2] = v.z; c.w[4 * p + 3] = v.w;
     }
     c.get2(f);
