@@ -105,6 +105,8 @@ def _geometry(grid, tile, windows):
 # ------------------------------------------------------------------ layer norm and dropout
 
 def _rows_cols(x, name: str):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if x.dim() < 1:
         raise ValueError(f"{name} must have at least one dimension")
     cols = int(x.shape[-1])
@@ -147,16 +149,24 @@ def sta_layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, residua
                            rng=None, stream=None):
     """``sta_layer_norm_fwd`` into new tensors: (y, h, mean, rstd).  ``h`` is None where
     it would be x itself (no residual and no dropout)."""
-    rows, _ = _rows_cols(x, "x")
-    with _On(stream, x):
+    rows, cols = _rows_cols(x, "x")
+    code = _dtype_code(x.dtype, "x")
+    with _On(stream, x, weight, bias, residual, rng) as st:   # new tensors need no checks of their own
+        w, b, pcode = _params(weight, bias, cols, x.dtype)
+        px, pr, prng = _ptr(x, "x"), _ptr(residual, "residual", x.dtype, x.shape, optional=True), _rng_ptr(rng)
         y = torch.empty_like(x)
         h = torch.empty_like(x) if residual is not None or dropout_p > 0 else None
-        mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
-    sta_layer_norm_fwd(x, weight, bias, y, eps, residual, h, mean, rstd, dropout_p, rng, stream)
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+        _check(load_library().sta_layer_norm_fwd(px, pr, w, b, y.data_ptr(), None if h is None else h.data_ptr(),
+                                                 mean.data_ptr(), rstd.data_ptr(), rows, cols, code, pcode, float(eps),
+                                                 float(dropout_p), prng, st), "sta_layer_norm_forward")
     return y, h, mean, rstd
 
 
+@functools.lru_cache(maxsize=256)
 def sta_layer_norm_bwd_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace that ``sta_layer_norm_bwd`` needs when it makes a weight's or bias's gradient."""
     n = load_library().sta_layer_norm_bwd_workspace(int(rows), int(cols))
     if n < 0:
         raise StaError(4, "sta_layer_norm_bwd_workspace")
@@ -195,14 +205,29 @@ def sta_layer_norm_backward(dy, h, mean, rstd, weight=None, dh=None, bias: bool 
     """``sta_layer_norm_bwd`` into new tensors: (dx, dresidual, dweight, dbias).  Without
     dropout dresidual is dx itself; dweight is None without a weight, dbias without
     ``bias``.  Both have the weight's type (h's type without a weight)."""
-    with _On(stream, h):
+    rows, cols = _rows_cols(h, "h")
+    code = _dtype_code(h.dtype, "h")
+    with _On(stream, dy, h, mean, rstd, weight, dh, rng) as st:   # new tensors need no checks of their own
+        w, _, pcode = _params(weight, None, cols, h.dtype)
+        like = h.dtype, h.shape
+        ptrs = [_ptr(dy, "dy", *like), _ptr(h, "h"), _ptr(mean, "mean", torch.float32, (rows,)),
+                _ptr(rstd, "rstd", torch.float32, (rows,)), w, _ptr(dh, "dh", *like, optional=True)]
+        prng = _rng_ptr(rng)
         dx = torch.empty_like(h)
         dres = torch.empty_like(h) if dropout_p > 0 else None
-        pd = h.dtype if weight is None else weight.dtype
-        cols = int(h.shape[-1])
-        dw = torch.empty(cols, dtype=pd, device=h.device) if weight is not None else None
-        db = torch.empty(cols, dtype=pd, device=h.device) if bias else None
-    sta_layer_norm_bwd(dy, h, mean, rstd, weight, dx, dres, dw, db, dh, dropout_p, rng, None, stream)
+        dw = db = ws = None
+        if weight is not None:
+            dw = torch.empty_like(weight)
+        if bias:
+            db = torch.empty(cols, dtype=h.dtype if weight is None else weight.dtype, device=h.device)
+        size = 0
+        if dw is not None or db is not None:
+            size = sta_layer_norm_bwd_workspace(rows, cols)
+            ws = torch.empty(size, dtype=torch.uint8, device=h.device)
+        ptrs += [None if t is None else t.data_ptr() for t in (dx, dres, dw, db)]
+        _check(load_library().sta_layer_norm_bwd(*ptrs, rows, cols, code, pcode, float(dropout_p), prng,
+                                                 None if ws is None else ws.data_ptr(), size, st),
+               "sta_layer_norm_backward")
     return dx, (dx if dres is None else dres), dw, db
 
 
@@ -219,9 +244,13 @@ def sta_dropout(x, y, dropout_p: float, rng, stream=None) -> None:
 
 def sta_dropout_forward(x, dropout_p: float, rng, stream=None):
     """``sta_dropout`` into a new tensor."""
-    with _On(stream, x):
+    rows, cols = _rows_cols(x, "x")
+    code = _dtype_code(x.dtype, "x")
+    with _On(stream, x, rng) as st:
+        px, prng = _ptr(x, "x"), _rng_ptr(rng)
         y = torch.empty_like(x)
-    sta_dropout(x, y, dropout_p, rng, stream)
+        _check(load_library().sta_dropout(px, y.data_ptr(), rows, cols, code, float(dropout_p), prng, st),
+               "sta_dropout_forward")
     return y
 
 
@@ -300,9 +329,17 @@ def sta_diff_forward(q, k, v, lam, grid, tile, window_per_head: Sequence, scale:
     1 / sqrt(d / 2), d / 2 being the columns of one map."""
     B, Hn, L, d = _diff_dims(q, grid, token_major, window_per_head)
     sc = 1.0 / math.sqrt(d / 2) if scale is None else float(scale)
-    with _On(stream, q):
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        out2 = torch.empty_like(out) if save else None
-        lse = torch.empty((2, B, Hn, L), dtype=torch.float32, device=q.device) if save else None
-    sta_diff_attention_fwd(q, k, v, lam, out, grid, tile, window_per_head, sc, out2, lse, token_major, stream)
+    geo = _geometry(grid, tile, window_per_head)
+    with _On(stream, q, k, v, lam) as st:   # new tensors need no checks of their own
+        shape = q.shape
+        ptrs = [_ptr(q, "q", torch.bfloat16), _ptr(k, "k", torch.bfloat16, shape), _ptr(v, "v", torch.bfloat16, shape),
+                _ptr(lam, "lam", torch.float32, (Hn,))]
+        out = torch.empty_like(q)
+        out2 = lse = None
+        if save:
+            out2 = torch.empty_like(q)
+            lse = torch.empty((2, B, Hn, L), dtype=torch.float32, device=q.device)
+        ptrs += [None if t is None else t.data_ptr() for t in (out, out2, lse)]
+        _check(load_library().sta_diff_attention_fwd(*ptrs, B, Hn, d, int(bool(token_major)), *geo, sc, st),
+               "sta_diff_forward")
     return (out, out2, lse) if save else out

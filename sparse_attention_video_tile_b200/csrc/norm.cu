@@ -411,8 +411,9 @@ cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t stream) {
 //   weight and bias read again for every row: 4580 and 5040 at 1024 columns, 4530 and 4430 at 1536;
 //   2048 and more: two rows a step 5520 and 5910, one 3840 and 4440 (4096: 5370 and 5440, 3600 and
 //   4030).  Above 4096 columns two fp32 rows with a residual do not fit in shared memory.
-// Rows that go through spans keep fewer threads a row up to 512 columns: there the reads from
-// shared memory bind, and 8 threads a row move 2880 and 5190 at 121 columns, 16 2290 and 3770.
+// Rows that go through spans have fewer threads a row up to 512 columns: their rows' ends and
+// barriers bind, and 8 threads a row move 2820 and 4340 at 121 columns, 16 2420 and 3450 (at 20 columns
+// two threads 2160 and 3930, four 1520 and 2840).
 template <typename T, bool VEC>
 cudaError_t pick_fwd(const NormFwdArgs& a, cudaStream_t stream) {
   constexpr bool k16 = sizeof(T) == 2;
@@ -468,59 +469,96 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T* __restrict__ x, T
   }
 }
 
-// Dropout, any number of columns: a thread takes eight consecutive elements of the
-// flat array (16-byte aligned), which lie in one or more rows, and evaluates every
-// counter block that they touch (two in most places).  Bound by the generator, which runs twice
-// per chunk: 3290 GB/s for rows that the kernel above takes at 5950; 80 M elements in rows of 1153
-// bf16 2120 GB/s, fp32 3760.
+// Dropout, any number of columns: a thread takes eight consecutive elements of the flat array
+// (16-byte aligned) at a time, four times, its warp 32 times as many side by side.  They lie in
+// two counter blocks in most places: that of their first element, which the thread evaluates, and
+// the next, which is the next thread's; what is not there (row ends, the warp's last thread)
+// is evaluated too.  Bound by the generator and the places' arithmetic: 72 754 x 1153 bf16 2580
+// GB/s, fp32 4240; with every block evaluated by each thread that needs it 2120 and 3760, and 4 to
+// 15 % more than here below 100 columns.
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_any_kernel(const T* __restrict__ x, T* __restrict__ y, int64_t total,
                                                           int32_t cols, const NormDropout drop) {
-  const int64_t e0 = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (e0 >= total) return;
-  const int n = total - e0 < 8 ? static_cast<int>(total - e0) : 8;
-  Chunk<T> c;
-  if (n == 8) c.load(x + e0); else c.load_n(x + e0, n);
+  constexpr int U = 4;
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const int64_t first = ((static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * (32 * U) + lane) * 8;
+  Chunk<T> c[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t e0 = first + u * 256;
+    if (e0 + 8 <= total) c[u].load(x + e0);
+    else if (e0 < total) c[u].load_n(x + e0, static_cast<int>(total - e0));
+  }
   if (drop.thr > 0) {
     const PhiloxKey key = philox_key(drop.rng);
     const uint32_t n8 = static_cast<uint32_t>((cols + 7) >> 3);
-    int64_t row;
-    int32_t col;
-    if (total <= 0x7fffffff) {
-      const uint32_t r = static_cast<uint32_t>(e0) / static_cast<uint32_t>(cols);
-      row = r;
-      col = static_cast<int32_t>(static_cast<uint32_t>(e0) - r * static_cast<uint32_t>(cols));
-    } else {
-      row = e0 / cols;
-      col = static_cast<int32_t>(e0 - row * cols);
-    }
-    uint32_t keep = 0;
-    for (int j = 0; j < n;) {
-      const uint32_t word = philox_keep(philox_block(static_cast<uint64_t>(row) * n8 + (col >> 3), key), drop.thr);
-      const int first = col & 7;
-      const int take = min(min(8 - first, cols - col), n - j);
-      keep |= ((word >> first) & ((1u << take) - 1u)) << j;
-      j += take;
-      col += take;
-      if (col == cols) {
-        col = 0;
-        ++row;
-      }
-    }
-    float f[8];
-    c.get(f);
+    int64_t row[U];
+    int32_t col[U];
+    uint32_t word[U];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = (keep >> e) & 1u ? f[e] * drop.scale : 0.f;
-    c.put(f);
+    for (int u = 0; u < U; ++u) {
+      const int64_t e0 = first + u * 256;
+      if (total <= 0x7fffffff) {   // then e0 fits 32 bits unsigned
+        const uint32_t r = static_cast<uint32_t>(e0) / static_cast<uint32_t>(cols);
+        row[u] = r;
+        col[u] = static_cast<int32_t>(static_cast<uint32_t>(e0) - r * static_cast<uint32_t>(cols));
+      } else {
+        row[u] = e0 / cols;
+        col[u] = static_cast<int32_t>(e0 - row[u] * cols);
+      }
+      word[u] = philox_keep(philox_block(static_cast<uint64_t>(row[u]) * n8 + (col[u] >> 3), key), drop.thr);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // the next thread's block: its number (low half, which tells neighbours apart) and bits
+      const uint32_t own = static_cast<uint32_t>(static_cast<uint64_t>(row[u]) * n8 + (col[u] >> 3));
+      uint32_t next = __shfl_down_sync(0xffffffffu, own, 1), bits = __shfl_down_sync(0xffffffffu, word[u], 1);
+      const int v = u + 1 < U ? u + 1 : u;
+      const uint32_t own0 = __shfl_sync(0xffffffffu, static_cast<uint32_t>(static_cast<uint64_t>(row[v]) * n8 + (col[v] >> 3)), 0);
+      const uint32_t word0 = __shfl_sync(0xffffffffu, word[v], 0);
+      if (lane == 31) {
+        next = own0;   // of the same step again where there is none after it: no later block, so it never matches
+        bits = word0;
+      }
+      const int64_t e0 = first + u * 256;
+      const int n = total - e0 < 8 ? static_cast<int>(total - e0) : 8;
+      uint32_t keep = 0;
+      int64_t r = row[u];
+      int32_t k = col[u];
+      for (int j = 0; j < n;) {
+        const uint64_t block = static_cast<uint64_t>(r) * n8 + (k >> 3);
+        uint32_t w = word[u];
+        if (j > 0) w = static_cast<uint32_t>(block) == next ? bits : philox_keep(philox_block(block, key), drop.thr);
+        const int at = k & 7;
+        const int take = min(min(8 - at, cols - k), n - j);
+        keep |= ((w >> at) & ((1u << take) - 1u)) << j;
+        j += take;
+        k += take;
+        if (k == cols) {
+          k = 0;
+          ++r;
+        }
+      }
+      float f[8];
+      c[u].get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = (keep >> e) & 1u ? f[e] * drop.scale : 0.f;
+      c[u].put(f);
+    }
   }
-  if (n == 8) c.store(y + e0); else c.store_n(y + e0, n);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t e0 = first + u * 256;
+    if (e0 + 8 <= total) c[u].store(y + e0);
+    else if (e0 < total) c[u].store_n(y + e0, static_cast<int>(total - e0));
+  }
 }
 
 template <typename T>
 cudaError_t dropout_t(const void* x, void* y, int64_t rows, int32_t cols, const NormDropout& drop, cudaStream_t stream) {
   const int64_t total = rows * cols;
   const bool flat = (cols & 7) == 0;
-  const int64_t per = flat ? 256 * 4 * 8 : 256 * 8;
+  constexpr int64_t per = 256 * 4 * 8;
   const int64_t blocks = (total + per - 1) / per;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (blocks < 1) return cudaSuccess;

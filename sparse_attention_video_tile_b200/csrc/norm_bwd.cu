@@ -13,7 +13,7 @@
 // Measured (a plain copy moves 6400 GB/s): 1 382 400 x 128 bf16 in 174 us, 6100 GB/s; 57 600 x
 // 1536 bf16 with the gradient that reaches h, dropout and both outputs in 180 us, 4900 GB/s, bound
 // by the generator's and the row's instructions at 16 warps an SM; fp32 4500 to 5900 GB/s; odd
-// widths from 9 columns on 1000 to 4000 GB/s (36 377 x 1153 bf16 2080, fp32 3210), bound by their
+// widths from 9 columns on 1000 to 4000 GB/s (36 377 x 1153 bf16 2190, fp32 3390), bound by their
 // passes through shared memory and the barriers.
 #include "norm_common.cuh"
 
@@ -509,6 +509,8 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
 //   chunk and two rows 5220 and 4870, 5210 and 4750;
 //   fp32 blocks: one chunk and two rows 6230 and 5490 at 1536 columns, 5230 and 4650 at 4096; two
 //   chunks of one row 5440 and 5740, 5860 and 5430; two and two 4090 and 3540 at 1536;
+//   odd widths, blocks: two rows 2190 and 3390 at 1153 columns, 2380 and 3310 at 2001; four 2080 and
+//   3230, 2210 and 2450;
 //   above 4096 columns: one block an SM 4570 and fp32 5690 at 5120 columns, two 4380 and 5440.
 struct BwdShape {
   int tpr, ch, rows, threads;
@@ -534,7 +536,7 @@ BwdShape bwd_shape(int64_t rows, int32_t cols, bool fp32) {
       s.rows = 1;
     } else if (!vec) {
       s.ch = 1;
-      s.rows = cols * (fp32 ? 4 : 2) <= 8192 ? 4 : 2;   // see bwd_t
+      s.rows = 2;
     } else {
       s.ch = fp32 && n8 <= 256 ? 1 : 2;
       s.rows = fp32 && n8 > 256 ? 1 : 2;
@@ -592,11 +594,7 @@ cudaError_t bwd_t(const NormBwdArgs& a, cudaStream_t stream) {
       default:
         if (s.ch == 2 && s.rows == 1) {
           e = launch_bwd<T, VEC, 0, 2, 1, 2>(a, s, stream);
-        } else if constexpr (!VEC) {
-          // through spans a step costs five barriers: four rows share them where they fit in shared
-          // memory (1153 columns: 1840 GB/s, fp32 2490; two rows 1550 and 1970)
-          e = s.rows == 4 ? launch_bwd<T, VEC, 0, 1, 4, 2>(a, s, stream) : launch_bwd<T, VEC, 0, 1, 2, 2>(a, s, stream);
-        } else if constexpr (sizeof(T) == 4) {
+        } else if constexpr (!VEC || sizeof(T) == 4) {
           e = launch_bwd<T, VEC, 0, 1, 2, 2>(a, s, stream);
         } else {
           e = launch_bwd<T, VEC, 0, 2, 2, 2>(a, s, stream);
