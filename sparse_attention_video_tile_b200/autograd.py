@@ -90,10 +90,19 @@ def sta_attention(q, k, v, grid, tile, window_per_head: Sequence, scale: Optiona
                                      [tuple(w) for w in window_per_head], float(scale), bool(token_major))
 
 
+def _dense(x):
+    """x as the kernels take it: contiguous from a 16-byte boundary.  A slice of rows of an odd
+    width, or its gradient, is contiguous and starts anywhere; it is copied."""
+    if x is None:
+        return None
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
 class STADiffAttentionFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, lam, grid, tile, windows, scale, token_major):
-        q, k, v, lam = (x.contiguous() for x in (q, k, v, lam))
+        q, k, v, lam = (_dense(x) for x in (q, k, v, lam))
         if not any(ctx.needs_input_grad):
             return sta_diff_forward(q, k, v, lam, grid, tile, windows, scale, token_major)
         out, out2, lse = sta_diff_forward(q, k, v, lam, grid, tile, windows, scale, token_major, save=True)
@@ -107,7 +116,7 @@ class STADiffAttentionFunction(torch.autograd.Function):
         q, k, v, lam, out, out2, lse = ctx.saved_tensors
         grid, tile, windows, scale, token_major = ctx.sta_args
         dq, dk, dv, dlam = (torch.empty_like(x) for x in (q, k, v, lam))
-        sta_diff_attention_bwd(q, k, v, lam, out, out2, lse, dout.to(torch.bfloat16).contiguous(), dq, dk, dv, dlam, grid,
+        sta_diff_attention_bwd(q, k, v, lam, out, out2, lse, _dense(dout.to(torch.bfloat16)), dq, dk, dv, dlam, grid,
                                tile, windows, scale, token_major)
         return dq, dk, dv, dlam, None, None, None, None, None
 
@@ -115,8 +124,7 @@ class STADiffAttentionFunction(torch.autograd.Function):
 class STALayerNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, residual, dropout_p, rng):
-        x = x.contiguous()
-        residual = None if residual is None else residual.contiguous()
+        x, residual, weight, bias = (_dense(t) for t in (x, residual, weight, bias))
         rng = rng.clone() if dropout_p > 0 else None   # the backward's mask, whatever becomes of the caller's state
         y, h, mean, rstd = sta_layer_norm_forward(x, weight, bias, eps, residual, dropout_p, rng)
         ctx.save_for_backward(x if h is None else h, mean, rstd, weight, rng)
@@ -128,8 +136,8 @@ class STALayerNormFunction(torch.autograd.Function):
     def backward(ctx, dy, dh=None):
         h, mean, rstd, weight, rng = ctx.saved_tensors
         has_bias, has_res, p, _, bias_dtype = ctx.sta_args
-        dy = dy.to(h.dtype).contiguous()
-        dh = None if dh is None else dh.to(h.dtype).contiguous()
+        dy = _dense(dy.to(h.dtype))
+        dh = None if dh is None else _dense(dh.to(h.dtype))
         want_w = weight is not None and ctx.needs_input_grad[1]
         want_b = has_bias and ctx.needs_input_grad[2]
         dx = torch.empty_like(h)
@@ -147,13 +155,13 @@ class STADropoutFunction(torch.autograd.Function):
         rng = rng.clone()
         ctx.save_for_backward(rng)
         ctx.dropout_p = dropout_p
-        return sta_dropout_forward(x.contiguous(), dropout_p, rng)
+        return sta_dropout_forward(_dense(x), dropout_p, rng)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         (rng,) = ctx.saved_tensors
-        return sta_dropout_forward(dy.contiguous(), ctx.dropout_p, rng), None, None
+        return sta_dropout_forward(_dense(dy), ctx.dropout_p, rng), None, None
 
 
 def _need_rng(dropout_p, rng):

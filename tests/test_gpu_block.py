@@ -112,6 +112,29 @@ def test_strided_and_half_precision_gradients_reach_the_leaves():
     assert torch.equal(out, saved[0]) and torch.equal(g, backward(q, k, v, lam, saved, do)[0])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_slices_that_start_off_a_16_byte_boundary(dtype):
+    """Rows of an odd width, sliced and joined again: the slices and the gradients that reach
+    them are contiguous and start anywhere.  The same values as aligned copies give."""
+    g = torch.Generator().manual_seed(5)
+    base, res, up = (torch.randn(9, 37, generator=g).to(dtype).cuda() for _ in range(3))
+    flat = torch.randn(1 + 2 * 37, generator=g).to(dtype).cuda()
+    rng = torch.tensor([3, 4], device="cuda")
+
+    def step(copy):
+        f = (lambda t: t.clone()) if copy else (lambda t: t)
+        x, r, w = (t.clone().requires_grad_() for t in (base, res, flat))
+        parts = []
+        for rows in (slice(0, 4), slice(4, 9)):
+            y, h = A.sta_layer_norm(f(x[rows]), f(w[1:38]), f(w[38:]), 1e-5, f(r[rows]), 0.25, rng)
+            parts.append(A.sta_dropout(f(y[1:]), 0.5, rng) + h[1:])
+        out = torch.cat(parts)
+        return (out,) + torch.autograd.grad(out, (x, r, w), up[:out.shape[0]])
+
+    for a, b in zip(step(False), step(True)):
+        assert torch.equal(a, b)
+
+
 def test_without_gradients_nothing_is_saved():
     q, k, v, _, lam = inputs(2)
     want = sta.sta_diff_forward(q, k, v, lam, GRID, TILE, WINDOWS, 0.18)
