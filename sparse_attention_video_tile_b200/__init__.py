@@ -91,6 +91,8 @@ def _d3(x: Sequence[int]) -> sta_dim3:
     t = tuple(int(v) for v in x)
     if len(t) != 3:
         raise ValueError(f"expected (t, h, w), got {x!r}")
+    if max(t) >= 2 ** 31 or min(t) < -2 ** 31:   # the fields are 32-bit, and ctypes would cut the value
+        raise ValueError(f"(t, h, w) must fit 32 bits, got {x!r}")
     return sta_dim3(*t)
 
 

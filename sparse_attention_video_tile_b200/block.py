@@ -20,6 +20,7 @@ import torch
 from . import StaError, _check, _d3, _stream, _stream_context, _windows, load_library
 
 
+_INT32_MAX = 2 ** 31 - 1
 _CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # sta_dtype
 
 
@@ -110,6 +111,8 @@ def _rows_cols(x, name: str):
     if x.dim() < 1:
         raise ValueError(f"{name} must have at least one dimension")
     cols = int(x.shape[-1])
+    if cols > _INT32_MAX:   # a 32-bit argument of the library, which ctypes would cut
+        raise ValueError(f"{name} must have fewer than 2^31 columns, got {cols}")
     return (int(x.numel()) // cols if cols else 0), cols
 
 
@@ -167,7 +170,8 @@ def sta_layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, residua
 @functools.lru_cache(maxsize=256)
 def sta_layer_norm_bwd_workspace(rows: int, cols: int) -> int:
     """Bytes of workspace that ``sta_layer_norm_bwd`` needs when it makes a weight's or bias's gradient."""
-    n = load_library().sta_layer_norm_bwd_workspace(int(rows), int(cols))
+    rows, cols = int(rows), int(cols)
+    n = load_library().sta_layer_norm_bwd_workspace(rows, cols) if rows < 2 ** 63 and abs(cols) <= _INT32_MAX else -1
     if n < 0:
         raise StaError(4, "sta_layer_norm_bwd_workspace")
     return int(n)
@@ -261,6 +265,8 @@ def _diff_dims(q, grid, token_major: bool, windows):
         raise ValueError("q must be [batch, heads, L, d], or [batch, L, heads, d] with token_major")
     a, b, c, d = q.shape
     B, Hn, L = (a, c, b) if token_major else (a, b, c)
+    if max(B, Hn, d) > _INT32_MAX:   # 32-bit arguments of the library, which ctypes would cut
+        raise ValueError(f"batch, heads and d must be below 2^31, got {B}, {Hn}, {d}")
     if L != grid[0] * grid[1] * grid[2]:
         raise ValueError("L must equal T*H*W")
     if len(windows) != Hn:

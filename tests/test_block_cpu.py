@@ -200,6 +200,33 @@ def test_norm_binding_checks(lib):
     assert A.sta_dropout(x, 0.0, None) is x
 
 
+def test_sizes_past_32_bits_are_refused_not_cut(lib):
+    """The library takes columns, heads, d, grids and windows as 32-bit numbers; a larger size
+    must not arrive as its low half (2^32 + 8 columns as 8)."""
+    x = torch.empty(2 ** 32 + 8, dtype=torch.bfloat16, device="meta")
+    rng = torch.zeros(2, dtype=torch.int64)
+    stat = torch.empty(1, device="meta")
+    for call in (lambda: sta.sta_dropout(x, x, 0.5, rng), lambda: sta.sta_dropout_forward(x, 0.5, rng),
+                 lambda: sta.sta_layer_norm_forward(x), lambda: sta.sta_layer_norm_fwd(x, None, None, x),
+                 lambda: sta.sta_layer_norm_bwd(x, x, stat, stat, None, x),
+                 lambda: sta.sta_layer_norm_backward(x, x, stat, stat)):
+        with pytest.raises(ValueError, match="columns"):
+            call()
+    for rows, cols in ((1, 2 ** 32 + 8), (2 ** 64 + 1, 8), (1, -2 ** 32 + 8)):
+        with pytest.raises(sta.StaError):
+            sta.sta_layer_norm_bwd_workspace(rows, cols)
+    q = torch.empty(1, 1, 1, 2 ** 32 + 64, dtype=torch.bfloat16, device="meta")
+    lam = torch.empty(1, device="meta")
+    with pytest.raises(ValueError, match="below 2\\^31"):
+        sta.sta_diff_forward(q, q, q, lam, (1, 1, 1), (6, 8, 8), [(1, 1, 1)])
+    small = torch.empty(1, 1, 384, 64, dtype=torch.bfloat16, device="meta")
+    for windows in ([(2 ** 32 + 1, 1, 1)], [(1, -2 ** 31 - 1, 1)]):
+        with pytest.raises(ValueError, match="32 bits"):
+            sta.sta_diff_forward(small, small, small, lam, (6, 8, 8), (6, 8, 8), windows)
+    with pytest.raises(ValueError, match="32 bits"):
+        sta.sta_attended_pairs(1, 1, (2 ** 32 + 6, 8, 8), (6, 8, 8), [(1, 1, 1)])
+
+
 def test_package_imports_without_the_block_module():
     with pytest.raises(AttributeError):
         sta.sta_no_such_operator
