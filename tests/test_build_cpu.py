@@ -18,7 +18,7 @@ def test_a_newer_file_makes_a_library_stale(name, tmp_path, monkeypatch):
     lib.write_bytes(b"")
     real = os.path.getmtime
     newer = os.path.join(B.CSRC, name)
-    built = max(real(os.path.join(B.CSRC, f)) for f in B.SOURCES + B.HEADERS) + 10
+    built = max(real(f) for f in [os.path.join(B.CSRC, f) for f in B.SOURCES + B.HEADERS] + [os.path.join(B.INCLUDE, "sta.h")]) + 10
     os.utime(lib, (built, built))
     assert not B._stale(str(lib))
     monkeypatch.setattr(os.path, "getmtime", lambda p: built + 1 if p == newer else real(p))
