@@ -388,7 +388,7 @@ cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t stream) {
   int sms = 0, dev = 0, fit = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = allow_smem(kern, 2 * R * 32 * 4);   // red
   if (e != cudaSuccess) return e;
   const int64_t need = ((a.rows + rows - 1) / rows + per_block - 1) / per_block;
   int64_t blocks = need;

@@ -564,7 +564,7 @@ cudaError_t launch_bwd(const NormBwdArgs& a, const BwdShape& s, cudaStream_t str
   const int stage = VEC ? R * CH * s.threads * 8 * static_cast<int>(sizeof(T))
                         : units * static_cast<int>(span_stage<T>(rows, a.cols));
   const int smem = STAGES * (a.dh != nullptr ? 3 : 2) * stage + (VEC ? 0 : kSpanSlack);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem(kern, 2 * R * 32 * 8 + (TPR > 0 ? 8 * 32 * CH * 8 * 4 : 0));   // red and acc
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(s.blocks), s.threads, smem, stream>>>(a);
   return cudaGetLastError();

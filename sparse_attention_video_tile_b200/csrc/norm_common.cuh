@@ -360,6 +360,16 @@ struct Own {
   }
 };
 
+// Allows a kernel all the dynamic shared memory that a block can have beside its static arrays
+// (at most `fixed` bytes).  The attribute belongs to the process, so every call sets the same
+// value, whatever it will use itself: with the call's own size, a call from another thread
+// could lower it between this thread's setting and its launch, which was then refused.
+constexpr int kSmemOptin = 227 * 1024;   // sm_100: a block's static and dynamic bytes
+template <typename F>
+inline cudaError_t allow_smem(F* kern, int fixed) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOptin - fixed);
+}
+
 // Barrier of the threads that share a span: a warp, or the block.
 template <bool BLOCK>
 __device__ __forceinline__ void span_sync() {

@@ -7,6 +7,8 @@ at most 80 u rstd max|h| |w| for the mean, the same relative size for rstd (half
 variance's 160 u) and a few u for the operations: 256 u (rstd max|h| + |z|) |w| + 4 u |b|
 covers them.  Every output adds half a step of its own type.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -253,3 +255,48 @@ def test_graph_replay_reads_the_generator_state_anew():
         torch.cuda.synchronize()
         f = B.dropout_factor(64, 256, 0.5, 5, off)
         assert np.array_equal(_np(y) == 0, f == 0)
+
+
+@pytest.mark.parametrize("cols", [1536, 3000, 4096, 837])
+def test_threads_with_unequal_calls_of_one_kernel(cols):
+    """Calls from several threads that need unequal amounts of shared memory of the same kernels:
+    with and without a residual (a gradient that reaches h), and at two widths of an instance.
+    They go to the C entry points with ready arguments, which leaves the interpreter's lock, so
+    that host code runs at the same time."""
+    lib, rows, rounds = sta.load_library(), 16, 3000
+    jobs, keep = [], []
+    for i in range(8):
+        c = cols - 8 * (i // 4)
+        x, r = (_rand((rows, c), torch.bfloat16, 10 * i + j).cuda() for j in (1, 2))
+        st = torch.cuda.Stream()
+        y, _, mean, rstd = sta.sta_layer_norm_forward(x, residual=r if i % 2 else None)
+        dx = sta.sta_layer_norm_backward(x, x, mean, rstd, None, r if i % 2 else None, False)[0]
+        out = [torch.empty_like(x) for _ in range(2)]
+        p = lambda t: t.data_ptr()  # noqa: E731
+        res, raw = (p(r) if i % 2 else None), st.cuda_stream
+        keep.append((x, r, y, mean, rstd, dx, out, st))
+        if i % 4 < 2:
+            jobs.append((lib.sta_layer_norm_fwd, (p(x), res, None, None, p(out[0]), None, None, None, rows, c, 0, 0, 1e-5, 0.0,
+                                                  None, raw)))
+        else:
+            jobs.append((lib.sta_layer_norm_bwd, (p(x), p(x), p(mean), p(rstd), None, res, p(out[1]), None, None, None, rows, c,
+                                                  0, 0, 0.0, None, None, 0, raw)))
+    torch.cuda.synchronize()
+    refused = []
+
+    def work(fn, args):
+        for _ in range(rounds):
+            status = fn(*args)
+            if status != sta.STA_OK:
+                refused.append((status, lib.sta_last_cuda_error()))
+                return
+
+    ts = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    assert not refused, refused
+    for i, (_, _, y, _, _, dx, out, _) in enumerate(keep):
+        assert torch.equal(out[0], y) if i % 4 < 2 else torch.equal(out[1], dx)
