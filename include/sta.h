@@ -326,6 +326,8 @@ sta_status sta_attention_fwd_noalloc(const void* q, const void* k, const void* v
  * captured graphs share no state but the status word.
  *   q, k, v, out: device bf16 in raster order, [batch, heads, L, d], or
  *     [batch, L, heads, d] with token_major = 1; 16-byte aligned;
+ *     The sums before the softmax's division are fp32 and reach 2^20 times a row's sum of
+ *     |v|: they stay finite where |v| is below 2^107 divided by the keys of the window;
  *   lambda: device fp32 [heads], any finite value;
  *   out2: device bf16 shaped like out, receives P_2 V, or NULL;
  *   lse: device fp32 [2, batch, heads, L] (raster order), receives the log-sum-exp

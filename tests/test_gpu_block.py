@@ -312,6 +312,26 @@ def test_very_low_and_very_high_scores():
         assert np.all(np.abs(gl[:, r] - lse[:, r]) <= 2.0 ** -9)
 
 
+def test_large_values_under_a_late_maximum():
+    """Values of 2^90 and a row whose last key scores 50 (in log2) above the rest: the sums before
+    the division must not be held against the first keys' maximum, and the order of the keys
+    must not matter."""
+    q, k, v, _, lam = inputs(16, batch=1, heads=1)
+    v = (v.float() * 2.0 ** 90).bfloat16()
+    q[0, 0, 3] = 0
+    q[0, 0, 3, 0], q[0, 0, 3, 32] = 12.0, 12.0
+    win = [(3, 2, 2)]
+    d = lambda t: t.double().cpu().numpy()  # noqa: E731
+    for key in (600, 1):
+        k[0, 0, :, 0], k[0, 0, :, 32] = 0, 0
+        k[0, 0, key, 0], k[0, 0, key, 32] = 16.0, 16.0
+        out, out2, _ = sta.sta_diff_forward(q, k, v, lam[:1], GRID, TILE, win, 0.18, save=True)
+        want, want2, _, bo, bo2 = B.diff_head(d(q[0, 0]), d(k[0, 0]), d(v[0, 0]), float(lam[0]), B.diff_mask(GRID, TILE, win[0]),
+                                              0.18)
+        assert torch.isfinite(out).all() and torch.isfinite(out2).all(), key
+        assert np.all(np.abs(d(out[0, 0]) - want) <= bo) and np.all(np.abs(d(out2[0, 0]) - want2) <= bo2), key
+
+
 def test_lambda_zero_negative_and_large():
     q, k, v, do, _ = inputs(15)
     d = lambda t: t.double().cpu().numpy()  # noqa: E731
