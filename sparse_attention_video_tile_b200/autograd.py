@@ -206,8 +206,9 @@ def sta_diff_attention(q, k, v, lam, grid, tile, window_per_head: Sequence, scal
     if scale is None:
         scale = 1.0 / float(q.shape[-1] // 2) ** 0.5
     _need_rng(dropout_p, rng)
-    out = STADiffAttentionFunction.apply(q, k, v, lam, tuple(grid), tuple(tile), [tuple(w) for w in window_per_head],
-                                         float(scale), bool(token_major))
+    # numbers of this call, whatever becomes of the caller's objects before the backward
+    grid, tile, windows = tuple(map(int, grid)), tuple(map(int, tile)), [tuple(map(int, w)) for w in window_per_head]
+    out = STADiffAttentionFunction.apply(q, k, v, lam, grid, tile, windows, float(scale), bool(token_major))
     if norm_weight is not None or norm_bias is not None:
         out = sta_layer_norm(out, norm_weight, norm_bias, eps)
     return sta_dropout(out, dropout_p, rng) if dropout_p > 0 else out

@@ -15,6 +15,7 @@ import functools
 import math
 from typing import Optional, Sequence
 
+import numpy as np
 import torch
 
 from . import StaError, _check, _d3, _stream, _stream_context, _windows, load_library
@@ -93,14 +94,21 @@ def _workspace_ptr(ws, name: str):
     return _ptr(ws, name), ws.numel() * ws.element_size()
 
 
-@functools.lru_cache(maxsize=64)
-def _geometry_args(grid, tile, windows):
-    """The C arguments of a (grid, tile, windows) triple; built once for each value."""
-    return _d3(grid), _d3(tile), _windows(windows)
+_GEOMETRIES = {}   # (grid, tile, windows) of plain numbers -> their C arguments
 
 
 def _geometry(grid, tile, windows):
-    return _geometry_args(tuple(grid), tuple(tile), tuple(map(tuple, windows)))
+    """The C arguments of a (grid, tile, windows) triple, built once for each value.  Only
+    numbers are kept: a tensor hashes by its identity, and its value can change."""
+    key = (tuple(grid), tuple(tile), tuple(map(tuple, windows)))
+    args = _GEOMETRIES.get(key)
+    if args is None:
+        args = _d3(key[0]), _d3(key[1]), _windows(key[2])
+        if all(isinstance(x, (int, np.integer)) for part in (key[:2], key[2]) for t in part for x in t):
+            if len(_GEOMETRIES) >= 64:
+                _GEOMETRIES.clear()
+            _GEOMETRIES[key] = args
+    return args
 
 
 # ------------------------------------------------------------------ layer norm and dropout

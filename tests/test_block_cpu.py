@@ -200,6 +200,56 @@ def test_norm_binding_checks(lib):
     assert A.sta_dropout(x, 0.0, None) is x
 
 
+def test_geometry_follows_values_that_change():
+    """The grid, tile and windows of a call are kept by value: a tensor that holds a number may
+    hold another one in the next call."""
+    from sparse_attention_video_tile_b200 import block
+    n, w = torch.tensor(4), torch.tensor([[1, 2, 3], [3, 2, 1]])
+    grid, windows = (n, 16, 16), [tuple(r) for r in w]
+    dims = lambda d: (d.t, d.h, d.w)  # noqa: E731
+    for a, b in ((4, 1), (7, 2)):
+        n.fill_(a)
+        w[0, 0] = b
+        g, _, ws = block._geometry(grid, (2, 8, 8), windows)
+        assert dims(g) == (a, 16, 16) and [dims(x) for x in ws] == [(b, 2, 3), (3, 2, 1)]
+    plain = block._geometry([4, 16, 16], (2, 8, 8), [[1, 2, 3]])
+    assert block._geometry((4, 16, 16), [2, 8, 8], ((1, 2, 3),)) is plain
+    assert block._geometry((np.int64(4), 16, 16), (2, 8, 8), np.array([[1, 2, 3]])) is plain
+    for i in range(200):
+        block._geometry((4, 16, 16 + i), (2, 8, 8), [(1, 2, 3)])
+    assert len(block._GEOMETRIES) <= 64
+
+
+class Recorder:
+    """Stands in for the binding under the autograd functions: keeps the calls' arguments and
+    returns tensors of the right shapes."""
+
+    def __init__(self, monkeypatch):
+        from sparse_attention_video_tile_b200 import autograd as A
+        self.A, self.forward, self.backward = A, [], []
+        monkeypatch.setattr(A, "sta_diff_forward", self.diff_forward)
+        monkeypatch.setattr(A, "sta_diff_attention_bwd", self.diff_backward)
+
+    def diff_forward(self, q, k, v, lam, *args, save=False, **kw):
+        self.forward.append((args, save))
+        return (q * 1, q * 1, torch.zeros(2, *q.shape[:3])) if save else q * 1
+
+    def diff_backward(self, *args, **kw):
+        self.backward.append(args[12:])
+        for g in args[8:12]:
+            g.zero_()
+
+
+def test_backward_uses_the_numbers_of_its_forward(monkeypatch):
+    rec = Recorder(monkeypatch)
+    q = torch.zeros(1, 1, 1024, 64, dtype=torch.bfloat16, requires_grad=True)
+    n = torch.tensor(4)
+    out = rec.A.sta_diff_attention(q, q, q, torch.zeros(1), (n, 16, 16), (2, 8, 8), [(n, 1, 1)])
+    n.fill_(7)
+    out.sum().backward()
+    assert rec.forward[0][0][:3] == rec.backward[0][:3] == ((4, 16, 16), (2, 8, 8), [(4, 1, 1)])
+
+
 def test_sizes_past_32_bits_are_refused_not_cut(lib):
     """The library takes columns, heads, d, grids and windows as 32-bit numbers; a larger size
     must not arrive as its low half (2^32 + 8 columns as 8)."""
