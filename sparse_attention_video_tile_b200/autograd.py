@@ -164,8 +164,10 @@ class STADropoutFunction(torch.autograd.Function):
         return sta_dropout_forward(_dense(dy), ctx.dropout_p, rng), None, None
 
 
-def _need_rng(dropout_p, rng):
-    if dropout_p > 0 and rng is None:
+def _check_dropout(dropout_p, rng):
+    if not 0.0 <= dropout_p <= 1.0:   # NaN too
+        raise ValueError(f"dropout_p must lie in 0 .. 1, got {dropout_p}")
+    if dropout_p > 0 and not isinstance(rng, torch.Tensor):
         raise ValueError("dropout needs rng, an int64 CUDA tensor [seed, offset]")
 
 
@@ -175,7 +177,7 @@ def sta_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, 
     Returns y, or (y, h) when there is a residual or dropout (h is the residual stream;
     its gradient flows back through the same kernel).  ``rng``: int64 CUDA tensor
     [seed, offset]; give each call of a step its own offset."""
-    _need_rng(dropout_p, rng)
+    _check_dropout(dropout_p, rng)
     return STALayerNormFunction.apply(x, weight, bias, float(eps), residual, float(dropout_p), rng)
 
 
@@ -183,9 +185,9 @@ def sta_dropout(x, dropout_p: float, rng):
     """Dropout with gradients; the mask is a function of ``rng`` (int64 CUDA tensor
     [seed, offset]) and the element's place (rows over the last dimension), and is
     evaluated again in the backward."""
+    _check_dropout(dropout_p, rng)
     if dropout_p == 0:
         return x
-    _need_rng(dropout_p, rng)
     return STADropoutFunction.apply(x, float(dropout_p), rng)
 
 
@@ -205,7 +207,7 @@ def sta_diff_attention(q, k, v, lam, grid, tile, window_per_head: Sequence, scal
     ``sta_dropout`` with ``rng``."""
     if scale is None:
         scale = 1.0 / float(q.shape[-1] // 2) ** 0.5
-    _need_rng(dropout_p, rng)
+    _check_dropout(dropout_p, rng)
     # numbers of this call, whatever becomes of the caller's objects before the backward
     grid, tile, windows = tuple(map(int, grid)), tuple(map(int, tile)), [tuple(map(int, w)) for w in window_per_head]
     out = STADiffAttentionFunction.apply(q, k, v, lam, grid, tile, windows, float(scale), bool(token_major))

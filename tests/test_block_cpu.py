@@ -250,6 +250,22 @@ def test_backward_uses_the_numbers_of_its_forward(monkeypatch):
     assert rec.forward[0][0][:3] == rec.backward[0][:3] == ((4, 16, 16), (2, 8, 8), [(4, 1, 1)])
 
 
+@pytest.mark.parametrize("p", [-0.1, 1.5, float("nan")])
+def test_a_probability_outside_its_range_is_refused(monkeypatch, p):
+    """By name and in every call, not taken as no dropout."""
+    rec = Recorder(monkeypatch)
+    q = torch.zeros(1, 1, 1024, 64, dtype=torch.bfloat16)
+    for rng in (None, torch.zeros(2, dtype=torch.int64)):
+        for call in (lambda: rec.A.sta_diff_attention(q, q, q, torch.zeros(1), (4, 16, 16), (2, 8, 8), [(1, 1, 1)],
+                                                      dropout_p=p, rng=rng),
+                     lambda: rec.A.sta_dropout(q, p, rng), lambda: rec.A.sta_layer_norm(q, dropout_p=p, rng=rng)):
+            with pytest.raises(ValueError, match="dropout_p"):
+                call()
+    assert not rec.forward
+    with pytest.raises(ValueError, match="rng"):
+        rec.A.sta_dropout(q, 0.5, [1, 2])
+
+
 def test_sizes_past_32_bits_are_refused_not_cut(lib):
     """The library takes columns, heads, d, grids and windows as 32-bit numbers; a larger size
     must not arrive as its low half (2^32 + 8 columns as 8)."""
