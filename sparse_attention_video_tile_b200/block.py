@@ -72,6 +72,9 @@ class _On:
                     raise ValueError(f"tensors of one call must be on one device, got {dev} and {d}")
         if dev is None or dev.type != "cuda":
             raise ValueError("CUDA tensors are required")
+        at = getattr(self.stream, "device", dev)   # a raw handle does not know its device
+        if at != dev:   # the kernels would run there, on memory of another device
+            raise ValueError(f"the stream is on {at}, the tensors are on {dev}")
         if self.stream is None and dev.index == torch.cuda.current_device():
             return torch._C._cuda_getCurrentRawStream(dev.index)
         with contextlib.ExitStack() as stack:

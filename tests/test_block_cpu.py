@@ -266,6 +266,21 @@ def test_a_probability_outside_its_range_is_refused(monkeypatch, p):
         rec.A.sta_dropout(q, 0.5, [1, 2])
 
 
+def test_a_stream_of_another_device_is_refused():
+    """Its kernels would run on that device and read this one's memory."""
+    from types import SimpleNamespace
+
+    from sparse_attention_video_tile_b200 import block
+
+    class OnGpu(torch.Tensor):
+        device = torch.device("cuda", 0)
+
+    x = torch.zeros(2, 8).as_subclass(OnGpu)
+    stream = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    with pytest.raises(ValueError, match="the stream is on cuda:1"):
+        block._On(stream, x, None).__enter__()
+
+
 def test_sizes_past_32_bits_are_refused_not_cut(lib):
     """The library takes columns, heads, d, grids and windows as 32-bit numbers; a larger size
     must not arrive as its low half (2^32 + 8 columns as 8)."""
