@@ -101,9 +101,9 @@ def _dense(x):
 
 class STADiffAttentionFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, lam, grid, tile, windows, scale, token_major):
+    def forward(ctx, q, k, v, lam, grid, tile, windows, scale, token_major, save):
         q, k, v, lam = (_dense(x) for x in (q, k, v, lam))
-        if not any(ctx.needs_input_grad):
+        if not save:
             return sta_diff_forward(q, k, v, lam, grid, tile, windows, scale, token_major)
         out, out2, lse = sta_diff_forward(q, k, v, lam, grid, tile, windows, scale, token_major, save=True)
         ctx.save_for_backward(q, k, v, lam, out, out2, lse)
@@ -118,7 +118,7 @@ class STADiffAttentionFunction(torch.autograd.Function):
         dq, dk, dv, dlam = (torch.empty_like(x) for x in (q, k, v, lam))
         sta_diff_attention_bwd(q, k, v, lam, out, out2, lse, _dense(dout.to(torch.bfloat16)), dq, dk, dv, dlam, grid,
                                tile, windows, scale, token_major)
-        return dq, dk, dv, dlam, None, None, None, None, None
+        return dq, dk, dv, dlam, None, None, None, None, None, None
 
 
 class STALayerNormFunction(torch.autograd.Function):
@@ -210,7 +210,10 @@ def sta_diff_attention(q, k, v, lam, grid, tile, window_per_head: Sequence, scal
     _check_dropout(dropout_p, rng)
     # numbers of this call, whatever becomes of the caller's objects before the backward
     grid, tile, windows = tuple(map(int, grid)), tuple(map(int, tile)), [tuple(map(int, w)) for w in window_per_head]
-    out = STADiffAttentionFunction.apply(q, k, v, lam, grid, tile, windows, float(scale), bool(token_major))
+    # here and not in the function's forward, where gradients are always off and needs_input_grad
+    # says what requires them whether or not they are
+    save = torch.is_grad_enabled() and any(x.requires_grad for x in (q, k, v, lam))
+    out = STADiffAttentionFunction.apply(q, k, v, lam, grid, tile, windows, float(scale), bool(token_major), save)
     if norm_weight is not None or norm_bias is not None:
         out = sta_layer_norm(out, norm_weight, norm_bias, eps)
     return sta_dropout(out, dropout_p, rng) if dropout_p > 0 else out

@@ -250,6 +250,20 @@ def test_backward_uses_the_numbers_of_its_forward(monkeypatch):
     assert rec.forward[0][0][:3] == rec.backward[0][:3] == ((4, 16, 16), (2, 8, 8), [(4, 1, 1)])
 
 
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode, torch.enable_grad])
+@pytest.mark.parametrize("leaf", [None, 0, 3])
+def test_saves_only_for_a_backward(monkeypatch, mode, leaf):
+    """out2 and the log-sum-exps are written where gradients are on and something requires one."""
+    rec = Recorder(monkeypatch)
+    t = [torch.zeros(1, 1, 1024, 64, dtype=torch.bfloat16) for _ in range(3)] + [torch.zeros(1)]
+    if leaf is not None:
+        t[leaf].requires_grad_(True)
+    want = leaf is not None and mode is torch.enable_grad
+    with mode():
+        out = rec.A.sta_diff_attention(*t, (4, 16, 16), (2, 8, 8), [(1, 1, 1)])
+    assert rec.forward[0][1] is want and out.requires_grad is want
+
+
 @pytest.mark.parametrize("p", [-0.1, 1.5, float("nan")])
 def test_a_probability_outside_its_range_is_refused(monkeypatch, p):
     """By name and in every call, not taken as no dropout."""
