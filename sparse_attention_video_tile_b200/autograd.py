@@ -124,6 +124,7 @@ class STADiffAttentionFunction(torch.autograd.Function):
 class STALayerNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps, residual, dropout_p, rng):
+        ctx.set_materialize_grads(False)   # h is often not used further: no zeros to write and read for its gradient
         x, residual, weight, bias = (_dense(t) for t in (x, residual, weight, bias))
         rng = rng.clone() if dropout_p > 0 else None   # the backward's mask, whatever becomes of the caller's state
         y, h, mean, rstd = sta_layer_norm_forward(x, weight, bias, eps, residual, dropout_p, rng)
@@ -136,7 +137,9 @@ class STALayerNormFunction(torch.autograd.Function):
     def backward(ctx, dy, dh=None):
         h, mean, rstd, weight, rng = ctx.saved_tensors
         has_bias, has_res, p, _, bias_dtype = ctx.sta_args
-        dy = _dense(dy.to(h.dtype))
+        if dy is None and dh is None:
+            return None, None, None, None, None, None, None
+        dy = torch.zeros_like(h) if dy is None else _dense(dy.to(h.dtype))
         dh = None if dh is None else _dense(dh.to(h.dtype))
         want_w = weight is not None and ctx.needs_input_grad[1]
         want_b = has_bias and ctx.needs_input_grad[2]

@@ -264,6 +264,29 @@ def test_saves_only_for_a_backward(monkeypatch, mode, leaf):
     assert rec.forward[0][1] is want and out.requires_grad is want
 
 
+@pytest.mark.parametrize("use", ["y", "h", "both"])
+def test_the_gradient_of_an_unused_output_is_not_made(monkeypatch, use):
+    """h = residual + dropout(x) is returned and often dropped: its gradient then stays None,
+    instead of zeros that the kernel reads."""
+    from sparse_attention_video_tile_b200 import autograd as A
+    seen = []
+    monkeypatch.setattr(A, "sta_layer_norm_forward",
+                        lambda x, w, b, eps, r, p, rng: (x * 1, x * 1, torch.zeros(4), torch.ones(4)))
+
+    def bwd(dy, h, mean, rstd, weight, dx, dres, dw, db, dh, p, rng):
+        seen.append((dy, dh))
+        dx.zero_()
+
+    monkeypatch.setattr(A, "sta_layer_norm_bwd", bwd)
+    x, r = (torch.randn(4, 8, requires_grad=True) for _ in range(2))
+    y, h = A.sta_layer_norm(x, residual=r)
+    sum({"y": [y], "h": [h], "both": [y, h]}[use]).sum().backward()
+    dy, dh = seen[0]
+    assert (dh is None) is (use == "y")
+    assert torch.equal(dy, torch.zeros(4, 8) if use == "h" else torch.ones(4, 8))
+    assert x.grad is not None and r.grad is not None
+
+
 @pytest.mark.parametrize("p", [-0.1, 1.5, float("nan")])
 def test_a_probability_outside_its_range_is_refused(monkeypatch, p):
     """By name and in every call, not taken as no dropout."""

@@ -145,6 +145,25 @@ def test_without_gradients_nothing_is_saved():
     assert torch.equal(out, want) and not out.requires_grad
 
 
+@pytest.mark.parametrize("p", [0.0, 0.25])
+def test_norm_gradients_by_either_output(p):
+    """Through y alone, h alone and both: the first two add up to the third within roundings,
+    and an unused h is worth a zero gradient, bit for bit."""
+    g = torch.Generator().manual_seed(3)
+    t = [torch.randn(9, 40, generator=g).cuda().requires_grad_() for _ in range(2)]
+    w, b = (torch.randn(40, generator=g).cuda().requires_grad_() for _ in range(2))
+    dy, dh = (torch.randn(9, 40, generator=g).cuda() for _ in range(2))
+    rng = torch.tensor([1, 2], device="cuda")
+    grads = lambda *o: torch.autograd.grad(*o, retain_graph=True, allow_unused=True)  # noqa: E731
+    y, h = A.sta_layer_norm(t[0], w, b, residual=t[1], dropout_p=p, rng=rng)
+    leaves = (*t, w, b)
+    by_y, by_h, by_both = grads(y, leaves, dy), grads(h, leaves, dh), grads((y, h), leaves, (dy, dh))
+    assert same(by_y, grads((y, h), leaves, (dy, torch.zeros_like(dh))))
+    for u, v, s in zip(by_y, by_h, by_both):
+        assert torch.allclose(u + v, s, rtol=0, atol=2.0 ** -20 * float(s.abs().max() + v.abs().max()))
+    assert not by_h[2].any() and not by_h[3].any()
+
+
 def test_second_derivative_raises():
     q, k, v, do, lam = inputs(2)
     q.requires_grad_(True)
