@@ -80,6 +80,7 @@ sta_status sta_layer_norm_fwd(const void* x, const void* residual, const void* w
   a.x = x; a.residual = residual; a.weight = weight; a.bias = bias;
   a.y = y; a.h = h; a.mean = mean; a.rstd = rstd;
   a.rows = rows; a.cols = cols; a.eps = eps;
+  a.n = static_cast<float>(cols); a.inv_n = 1.0f / a.n;
   a.wfp32 = param_dtype == STA_FP32;
   return finish(launch_norm_fwd(dtype, a, static_cast<cudaStream_t>(stream)));
 }

@@ -21,6 +21,16 @@ namespace {
 
 using namespace norm;
 
+// s / n from s and 1 / n: the product, and what it lacks of s, s - q n, which an fma gives without
+// rounding, divided in the same way.  The sum of up to 8192 equal bf16 or fp16 values is exact in
+// fp32, and so is their mean then: a constant row's y is the bias (with the product alone, 1 / n's
+// rounding times 1 / sqrt(eps)).  The two fma cost nothing without dropout and 2 to 3 % with it,
+// where the vector kernels leave them out; a division took 2 to 13 % of the bf16 kernels' time.
+__device__ __forceinline__ float mean_of(float s, float n, float inv_n) {
+  const float q = s * inv_n, r = fmaf(-q, n, s);
+  return fmaf(r == r ? r : 0.f, inv_n, q);   // an infinite sum stays one
+}
+
 // TPR threads share a row (0: the whole block); a thread holds CH chunks of R rows at a
 // time.  A warp (or block) takes consecutive rows; STAGES - 1 of its steps are on their way
 // to shared memory while one is in registers, so the bytes in flight do not depend on the
@@ -47,7 +57,6 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
   T* h = static_cast<T*>(a.h);
   PhiloxKey key{};
   if (a.drop.thr > 0) key = philox_key(a.drop.rng);
-  const float inv_n = 1.0f / static_cast<float>(a.cols);
   const uint32_t one = span_stage<T>(kRows, a.cols), stage = res != nullptr ? 2 * one : one;
   uint8_t* mine = bufs + (kBlock ? 0 : (threadIdx.x >> 5) * STAGES * stage);
   uint64_t w[CH][4], b[CH][4];   // they stay in registers
@@ -122,7 +131,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
       for (int k = 0; k < CH; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i & 1] = add_f32x2(s[i & 1], f[r][k][i]);   // columns past the row hold zero
-      mean[r] = row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[0][r]) * inv_n;
+      mean[r] = mean_of(row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[0][r]), a.n, a.inv_n);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -147,7 +156,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_fwd_kernel(const Nor
           }
         }
       }
-      rstd[r] = rsqrtf(fmaf(row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[1][r]), inv_n, a.eps));
+      rstd[r] = rsqrtf(fmaf(row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[1][r]), a.inv_n, a.eps));
     }
     // rows out: h as it is, y normalised
 #pragma unroll
@@ -235,7 +244,6 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 && CH <= 2 ? 2 : 
   const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(bufs)) + 16 * threadIdx.x;
   PhiloxKey key{};
   if (DROP) key = philox_key(a.drop.rng);
-  const float inv_n = 1.0f / static_cast<float>(a.cols);
   const int psize = a.wfp32 ? 4 : static_cast<int>(sizeof(T)), p_bytes = step * 8 * psize;
   const char* wp = static_cast<const char*>(a.weight) + lane * 8 * psize;   // this thread's first parameters
   const char* bp = static_cast<const char*>(a.bias) + lane * 8 * psize;
@@ -317,7 +325,8 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 && CH <= 2 ? 2 : 
       for (int k = 0; k < CH; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i & 1] = add_f32x2(s[i & 1], f[r][k][i]);   // missing chunks hold zero
-      mean[r] = row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[0][r]) * inv_n;
+      const float t = row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[0][r]);
+      mean[r] = DROP ? t * a.inv_n : mean_of(t, a.n, a.inv_n);   // a row with dropped values is not constant
     }
     if (a.h != nullptr) {
 #pragma unroll
@@ -339,7 +348,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512, TPR > 0 && CH <= 2 ? 2 : 
           s[i & 1] = fma_f32x2(f[r][k][i], f[r][k][i], s[i & 1]);
         }
       }
-      rstd[r] = rsqrtf(fmaf(row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[1][r]), inv_n, a.eps));
+      rstd[r] = rsqrtf(fmaf(row_sum<TPR>(sum_f32x2(add_f32x2(s[0], s[1])), red[1][r]), a.inv_n, a.eps));
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) {

@@ -22,6 +22,7 @@ struct NormFwdArgs {
   float *mean, *rstd;
   int64_t rows;
   int32_t cols;
+  float n, inv_n;   // cols and 1 / cols: operands from the parameters take no registers
   float eps;
   bool wfp32;
   NormDropout drop;

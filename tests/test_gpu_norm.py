@@ -225,6 +225,23 @@ def test_constant_row_and_nonfinite_rows_stay_apart():
     assert np.abs(y[[0, 4]].double().numpy() - want).max() < 1e-5
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("cols", [3, 7, 24, 37, 121, 257, 600, 837, 1153, 1999, 3000, 5000, 8190])
+def test_constant_rows_are_the_bias(cols, dtype):
+    """A row of one 16-bit value at any width: its sum is exact in fp32 (8 or 11 bits times at most
+    13), the mean is that value, and y is the bias, not a rounding of the mean times 1 / sqrt(eps)."""
+    dt = TYPES[dtype]
+    x = _rand((40, 1), dt, 9, 200.0).expand(40, cols).contiguous().cuda()
+    b = _rand((cols,), dt, 10).cuda()
+    y, _, mean, rstd = sta.sta_layer_norm_forward(x, None, b, 1e-5)
+    assert torch.equal(mean, x[:, 0].float())
+    assert torch.equal(y, b.expand(40, cols))
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=2.0 ** -20, atol=0)
+    x[3, 0] = float("inf")
+    _, _, mean, rstd = sta.sta_layer_norm_forward(x, None, b, 1e-5)
+    assert mean[3] == float("inf") and torch.isnan(rstd[3]) and torch.isfinite(mean[4:]).all()
+
+
 def test_deterministic_and_on_another_stream():
     h, dy = (_rand((5000, 300), torch.bfloat16, i).cuda() for i in (1, 2))
     w = _rand((300,), torch.float32, 3).cuda()
