@@ -328,7 +328,8 @@ sta_status sta_attention_fwd_noalloc(const void* q, const void* k, const void* v
  *     [batch, L, heads, d] with token_major = 1; 16-byte aligned;
  *     The sums before the softmax's division are fp32 and reach 2^20 times a row's sum of
  *     |v|: they stay finite where |v| is below 2^107 divided by the keys of the window;
- *   lambda: device fp32 [heads], any finite value;
+ *   lambda: device fp32 [heads], any value for which lambda P_2 V and its gradients are
+ *     finite.  |lambda| far above 1 costs the backward accuracy, see there;
  *   out2: device bf16 shaped like out, receives P_2 V, or NULL;
  *   lse: device fp32 [2, batch, heads, L] (raster order), receives the log-sum-exp
  *     of scale * Q_m K_m^T over each row's window (natural log), or NULL.  The
@@ -357,7 +358,11 @@ sta_status sta_diff_attention_fwd(const void* q, const void* k, const void* v, c
  *   dlambda[h] = - sum over batch and rows of D_2 (fp32, the sum taken from P_2 and
  *   dP in fp32).
  * P is rebuilt from lse; the products take P and dS rounded to bf16 and accumulate
- * in fp32.  dq, dk, dv: device bf16 laid out like q; dlambda: device fp32 [heads].
+ * in fp32.  D_2 is dO . out2 and D_1 is dO . out + lambda dO . out2, from the stored bf16
+ * rows: D_1 is off by up to 2^-8 sum |dO| (|out| + |lambda| |out2|), which grows with
+ * |lambda| while D_1 does not.  Map 1's dQ and dK lose accuracy in that proportion (at
+ * lambda = 3 about three times the error of lambda below 1, at 100 about a hundred
+ * times); map 2's scale with lambda, and dV and dlambda are not touched.  dq, dk, dv: device bf16 laid out like q; dlambda: device fp32 [heads].
  * Every output element is written.  Deterministic: no atomics.
  *   workspace: device memory of at least sta_diff_attention_bwd_workspace(...) bytes,
  *     16-byte aligned, used until the call's kernels have run.  Calls that may overlap

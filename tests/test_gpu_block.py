@@ -371,6 +371,27 @@ def test_lambda_zero_negative_and_large():
     assert not grads[0][:, 0, :, 32:].any()    # lambda 0: the second map has no gradient
 
 
+def test_lambda_far_above_one():
+    """The stated accuracy at |lambda| = 30 and 100: the bound on the first map's dq and dk holds D_1's
+    term that grows with |lambda|; the second map's grows as these gradients themselves do."""
+    q, k, v, do, _ = inputs(17)
+    d = lambda t: t.double().cpu().numpy()  # noqa: E731
+    lam = torch.tensor([30.0, -100.0, 0.5], device="cuda")
+    saved = sta.sta_diff_forward(q, k, v, lam, GRID, TILE, WINDOWS, 0.18, save=True)
+    grads = backward(q, k, v, lam, saved, do)
+    for h in range(3):
+        mask = B.diff_mask(GRID, TILE, WINDOWS[h])
+        dl = bl = 0.0
+        for b in range(2):
+            want, _, _, bo, _ = B.diff_head(d(q[b, h]), d(k[b, h]), d(v[b, h]), float(lam[h]), mask, 0.18)
+            assert np.all(np.abs(d(saved[0][b, h]) - want) <= bo)
+            w, bd = B.diff_head_backward(d(q[b, h]), d(k[b, h]), d(v[b, h]), float(lam[h]), d(do[b, h]), mask, 0.18)
+            for g, x, y in zip(grads, w[:3], bd[:3]):
+                assert np.all(np.abs(d(g[b, h]) - x) <= y)
+            dl, bl = dl + w[3], bl + bd[3]
+        assert abs(float(grads[3][h]) - dl) <= bl
+
+
 def test_empty_batch():
     q = torch.empty(0, 2, 630, 64, device="cuda", dtype=torch.bfloat16)
     lam = torch.rand(2, device="cuda")
