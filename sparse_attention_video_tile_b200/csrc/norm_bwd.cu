@@ -499,9 +499,12 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
 }
 
 // Launch shape of the first kernel: threads that share a row (0: the block), chunks of a
-// thread, rows of a block's step, threads of a block, blocks.  It depends on the sizes and the
-// type alone, and so do the parts and the sums' order.  No more blocks than an SM holds (128
-// registers a thread, 168 where a thread has two chunks of two rows).  Rates of plain calls over
+// thread, rows of a block's step, threads of a block, blocks.  It depends on the sizes, the type
+// and whether dh is given, and so do the parts and the sums' order.  No more blocks than an SM
+// holds, by registers here (128 a thread, 168 where a thread has two chunks of two rows) and by shared
+// memory in launch_bwd: fp32 warps with their stages of two or three arrays often fill an SM with one
+// block, and a grid of two waves took 1 to 4 % longer (58 M elements x 64 columns with dh 163 and 158 us).
+// Rates of plain calls over
 // 170 M elements and of calls with every option over 85 M, in GB/s:
 //   1024 columns: a warp a row, one block an SM: bf16 6000 and 5880, fp32 5700 and 4930; a block a
 //   row: 5390 and 4800, 5980 and 4510;
@@ -552,7 +555,7 @@ BwdShape bwd_shape(int64_t rows, int32_t cols, bool fp32) {
 }
 
 template <typename T, bool VEC, int TPR, int CH, int R, int STAGES>
-cudaError_t launch_bwd(const NormBwdArgs& a, const BwdShape& s, cudaStream_t stream) {
+cudaError_t launch_bwd(const NormBwdArgs& a, BwdShape& s, cudaStream_t stream) {
   void (*kern)(NormBwdArgs);
   if constexpr (VEC)
     kern = a.drop.thr > 0 ? norm_bwd_vec_kernel<T, true, TPR, CH, R, STAGES>
@@ -564,7 +567,10 @@ cudaError_t launch_bwd(const NormBwdArgs& a, const BwdShape& s, cudaStream_t str
   const int stage = VEC ? R * CH * s.threads * 8 * static_cast<int>(sizeof(T))
                         : units * static_cast<int>(span_stage<T>(rows, a.cols));
   const int smem = STAGES * (a.dh != nullptr ? 3 : 2) * stage + (VEC ? 0 : kSpanSlack);
-  const cudaError_t e = allow_smem(kern, 2 * R * 32 * 8 + (TPR > 0 ? 8 * 32 * CH * 8 * 4 : 0));   // red and acc
+  constexpr int fixed = 2 * R * 32 * 8 + (TPR > 0 ? 8 * 32 * CH * 8 * 4 : 0);   // red and acc
+  const int fit = kSmemSm / (smem + fixed + kSmemBlock);
+  if (s.blocks > 148 * fit) s.blocks = 148 * fit;
+  const cudaError_t e = allow_smem(kern, fixed);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(s.blocks), s.threads, smem, stream>>>(a);
   return cudaGetLastError();
@@ -572,7 +578,7 @@ cudaError_t launch_bwd(const NormBwdArgs& a, const BwdShape& s, cudaStream_t str
 
 template <typename T, bool VEC>
 cudaError_t bwd_t(const NormBwdArgs& a, cudaStream_t stream) {
-  const BwdShape s = bwd_shape(a.rows, a.cols, sizeof(T) == 4);
+  BwdShape s = bwd_shape(a.rows, a.cols, sizeof(T) == 4);
   if (a.rows > 0) {
     cudaError_t e;
     switch (s.tpr) {

@@ -365,6 +365,7 @@ struct Own {
 // value, whatever it will use itself: with the call's own size, a call from another thread
 // could lower it between this thread's setting and its launch, which was then refused.
 constexpr int kSmemOptin = 227 * 1024;   // sm_100: a block's static and dynamic bytes
+constexpr int kSmemSm = 228 * 1024, kSmemBlock = 1024;   // an SM's, and what it takes of them for a block
 template <typename F>
 inline cudaError_t allow_smem(F* kern, int fixed) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOptin - fixed);
