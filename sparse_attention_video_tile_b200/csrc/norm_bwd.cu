@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
 // and whether dh is given, and so do the parts and the sums' order.  No more blocks than an SM
 // holds, by registers here (128 a thread, 168 where a thread has two chunks of two rows) and by shared
 // memory in launch_bwd: fp32 warps with their stages of two or three arrays often fill an SM with one
-// block, and a grid of two waves took 1 to 4 % longer (58 M elements x 64 columns with dh 163 and 158 us).
+// block, and a grid of two waves took 1 to 4 % longer (937 500 x 64 with dh 163 and 158 us).
 // Rates of plain calls over
 // 170 M elements and of calls with every option over 85 M, in GB/s:
 //   1024 columns: a warp a row, one block an SM: bf16 6000 and 5880, fp32 5700 and 4930; a block a
