@@ -207,9 +207,10 @@ def sta_diff_attention(q, k, v, lam, grid, tile, window_per_head: Sequence, scal
     proportion to it, since their row sums come from the stored bf16 outputs.
 
     With ``norm_weight`` (and ``norm_bias``), both [d], every head's output row then
-    goes through ``sta_layer_norm``, as the method normalises its heads (a factor such as
-    1 - lambda_init belongs in the weight), and with ``dropout_p`` > 0 through
-    ``sta_dropout`` with ``rng``."""
+    goes through ``sta_layer_norm`` (a factor such as 1 - lambda_init belongs in the weight).
+    The published method has an RMS norm there, without the mean and a bias: weights trained
+    with that one give other numbers here.  With ``dropout_p`` > 0 the result
+    goes through ``sta_dropout`` with ``rng``."""
     if scale is None:
         scale = 1.0 / float(q.shape[-1] // 2) ** 0.5
     _check_dropout(dropout_p, rng)
