@@ -164,7 +164,7 @@ __device__ __forceinline__ void sum_dlambda(const DiffGeo& g, const float* part,
 // in columns of their own (256-383), dQ_1 and dQ_2 (384-511).  Scores are free again
 // once they are in registers and dP once both maps have read it, so the next block's
 // S and dP run under this block's exponentials.  Bound by that chain of the elementwise
-// warps, 3760 clocks a block.  Measured, 6 heads of 115 200 tokens, windows of 27 tiles of 384:
+// warps, 3547 clocks a block (ncu, active cycles; 1.69 GHz).  Measured, 6 heads of 115 200 tokens, windows of 27 tiles of 384:
 // 5.84 ms at d = 128, 5.28 at d = 64 (5.42 with two stages of K and V instead of four).
 
 template <int D>
@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // -lse and -D of a query block are loaded apart from Q and dO, each into one buffer: -lse
 // is free after the exponentials, -D after dS, and each is needed again half a block later.
 // Bound by the elementwise warps: exponentials of both maps, then dP, the three operands and
-// their stores, 5000 clocks a block, under which the products run.  Measured at the sizes above:
+// their stores, 4571 clocks a block (ncu, active cycles; 1.59 GHz), under which the products
+// run.  Measured at the sizes above:
 // 7.85 ms at d = 128, 7.4 at d = 64; 10.1 with a row per thread, 8.1 to 9.2 with 2 to 4 of 8
 // exponentials on the FMA pipe.
 

@@ -31,8 +31,9 @@
 // the other attention kernels), l is summed from the unrounded p.
 //
 // Bound: one warp's serial chain per block (scores into registers, maximum, 128
-// exponentials a thread, P out), 3100 clocks, against 2048 of MUFU and 1860 of tensor
-// work (M128 N128 K16 takes 64 clocks, N64 52).  Measured on 115 200 tokens, windows of 27
+// exponentials a thread, P out), 2626 clocks (active cycles counted by ncu over 1313.5 blocks
+// an SM, d = 128), against 2048 of MUFU (78 %) and 1536 of tensor work (24 M128 N128 K16 of 64
+// clocks, 58.5 %); the rest of the time is the clock under the power cap, 1.62 GHz.  Measured on 115 200 tokens, windows of 27
 // tiles of 384: d = 128, 24 heads 20.1 ms, 710 TFLOP/s counting 4 d a pair (12 heads 10.0);
 // d = 64, 12 heads 8.8 ms.  Sixteen softmax warps with half rows take 10.85 and 9.5 ms at 12
 // heads, P stored in parts as it is made 11.6 and 9.8, 2 or 4 of 8 pairs of exponentials on
