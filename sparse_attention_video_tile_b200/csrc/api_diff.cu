@@ -4,31 +4,11 @@
 #include <cfloat>
 #include <cmath>
 
+#include "checks.h"
 #include "diff.h"
 
 namespace sta {
 namespace {
-
-struct Range {
-  const void* p;
-  int64_t bytes;
-};
-
-bool overlap(const Range& a, const Range& b) {
-  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
-}
-
-// Whether any of the first n_out ranges overlaps another one.
-bool any_overlap(const Range* r, int n_out, int n) {
-  for (int i = 0; i < n_out; ++i)
-    for (int j = 0; j < n; ++j)
-      if (j != i && overlap(r[i], r[j])) return true;
-  return false;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
@@ -136,8 +116,8 @@ sta_status sta_diff_attention_fwd(const void* q, const void* k, const void* v, c
   if (bh == 0) return STA_OK;
   if (!q || !k || !v || !lambda || !out) return STA_ERR_NULL;
   for (const void* p : {q, k, v, static_cast<const void*>(out), static_cast<const void*>(out2)})
-    if (!aligned16(p)) return STA_ERR_ALIGN;
-  if (reinterpret_cast<uintptr_t>(lse) % 4 != 0 || reinterpret_cast<uintptr_t>(lambda) % 4 != 0) return STA_ERR_ALIGN;
+    if (!aligned_to(p, 16)) return STA_ERR_ALIGN;
+  if (!aligned_to(lse, 4) || !aligned_to(lambda, 4)) return STA_ERR_ALIGN;
   const int64_t n = bh * g.L * d * 2;
   const Range r[] = {{out, n}, {out2, n}, {lse, 2 * bh * g.L * 4}, {q, n}, {k, n}, {v, n}, {lambda, heads * 4}};
   if (any_overlap(r, 3, 7)) return STA_ERR_ALIAS;
@@ -169,9 +149,9 @@ sta_status sta_diff_attention_bwd(const void* q, const void* k, const void* v, c
     return STA_ERR_NULL;
   for (const void* p : {q, k, v, out, out2, dout, static_cast<const void*>(dq), static_cast<const void*>(dk),
                         static_cast<const void*>(dv), static_cast<const void*>(workspace)})
-    if (!aligned16(p)) return STA_ERR_ALIGN;
+    if (!aligned_to(p, 16)) return STA_ERR_ALIGN;
   for (const float* p : {lambda, lse, static_cast<const float*>(dlambda)})
-    if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return STA_ERR_ALIGN;
+    if (!aligned_to(p, 4)) return STA_ERR_ALIGN;
   const BwdLayout l = bwd_layout(g, d);
   if (bh > 0 && workspace_bytes < l.total) return STA_ERR_SCRATCH;
   const int64_t n = bh * g.L * d * 2;

@@ -2,32 +2,12 @@
 // argument checks, then one or two kernel launches on the caller's stream.
 #include <cmath>
 
+#include "checks.h"
 #include "internal.h"
 #include "norm.h"
 
 namespace sta {
 namespace {
-
-struct Range {
-  const void* p;
-  int64_t bytes;
-};
-
-bool overlap(const Range& a, const Range& b) {
-  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
-}
-
-// Whether any of the first n_out ranges overlaps another one.
-bool any_overlap(const Range* r, int n_out, int n) {
-  for (int i = 0; i < n_out; ++i)
-    for (int j = 0; j < n; ++j)
-      if (j != i && overlap(r[i], r[j])) return true;
-  return false;
-}
-
-bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int64_t dtype_size(int32_t dtype) { return dtype == STA_FP32 ? 4 : 2; }
 
