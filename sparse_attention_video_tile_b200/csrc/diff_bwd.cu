@@ -36,12 +36,6 @@ constexpr int kRegsOther = 56;
 static_assert(256 * kRegsElem + 128 * kRegsOther <= kThreads * 168, "register split above the launch allocation");
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 struct BwdParams {
   DiffGeo g;
   const float* lam;

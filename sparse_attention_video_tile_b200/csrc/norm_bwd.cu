@@ -49,6 +49,62 @@ __device__ __forceinline__ void row_sum2(float& u, float& v, float2* red) {
   }
 }
 
+// Writes this block's part of the column sums: dw at partial[block], db at partial[blocks + block].
+// A thread's sums are of chunks lane, lane + step, ... (every thread of the block calls it).
+template <int TPR, int CH>
+__device__ __forceinline__ void store_column_sums(const NormBwdArgs& a, const uint64_t (&dw)[CH][4], const uint64_t (&db)[CH][4],
+                                                  int lane, int step) {
+  if (a.partial == nullptr) return;
+  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
+  float* pb = pw + static_cast<int64_t>(gridDim.x) * a.cols;
+  if constexpr (TPR > 0) {
+    // the block's groups: those of a warp by shuffles, the warps through shared memory
+    __shared__ float acc[8][32 * CH * 8];
+    const int warp = static_cast<int>(threadIdx.x) >> 5;
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass) __syncthreads();
+#pragma unroll
+      for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float u[2];
+          f32x2_split(pass ? db[k][i] : dw[k][i], u[0], u[1]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int o = 16; o >= TPR; o >>= 1) u[j] += __shfl_xor_sync(0xffffffffu, u[j], o);
+            if ((static_cast<int>(threadIdx.x) & 31) < TPR) acc[warp][(lane + k * TPR) * 8 + 2 * i + j] = u[j];
+          }
+        }
+      __syncthreads();
+      for (int32_t c = static_cast<int32_t>(threadIdx.x); c < a.cols; c += 256) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += acc[q][c];
+        (pass ? pb : pw)[c] = s;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int32_t c0 = (lane + k * step) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float u[2], v[2];
+        f32x2_split(dw[k][i], u[0], u[1]);
+        f32x2_split(db[k][i], v[0], v[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (c0 + 2 * i + j < a.cols) {
+            pw[c0 + 2 * i + j] = u[j];
+            pb[c0 + 2 * i + j] = v[j];
+          }
+      }
+    }
+  }
+}
+
 // TPR threads share a row (0: the whole block); a thread holds CH chunks of R rows at a
 // time, while the next STAGES - 1 steps of its warp (block) are on their way to shared memory.
 template <typename T, int TPR, int CH, int R, int STAGES>
@@ -220,55 +276,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 512) norm_bwd_kernel(const Nor
     slot = slot + 1 == STAGES ? 0 : slot + 1;
   }
   span_wait<0>();
-  if (a.partial == nullptr) return;
-  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
-  float* pb = pw + static_cast<int64_t>(gridDim.x) * a.cols;
-  if constexpr (TPR > 0) {
-    // the block's groups: those of a warp by shuffles, the warps through shared memory
-    __shared__ float acc[8][32 * CH * 8];
-    const int warp = static_cast<int>(threadIdx.x) >> 5;
-#pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      if (pass) __syncthreads();
-#pragma unroll
-      for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float u[2];
-          f32x2_split(pass ? db[k][i] : dw[k][i], u[0], u[1]);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int o = 16; o >= TPR; o >>= 1) u[j] += __shfl_xor_sync(0xffffffffu, u[j], o);
-            if ((static_cast<int>(threadIdx.x) & 31) < TPR) acc[warp][(lane + k * TPR) * 8 + 2 * i + j] = u[j];
-          }
-        }
-      __syncthreads();
-      for (int32_t c = static_cast<int32_t>(threadIdx.x); c < a.cols; c += 256) {
-        float s = 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) s += acc[q][c];
-        (pass ? pb : pw)[c] = s;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int32_t c0 = (lane + k * step) * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float u[2], v[2];
-        f32x2_split(dw[k][i], u[0], u[1]);
-        f32x2_split(db[k][i], v[0], v[1]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (c0 + 2 * i + j < a.cols) {
-            pw[c0 + 2 * i + j] = u[j];
-            pb[c0 + 2 * i + j] = v[j];
-          }
-      }
-    }
-  }
+  store_column_sums<TPR, CH>(a, dw, db, lane, step);
 }
 
 // The same for rows of a multiple of eight columns (see Own).
@@ -418,55 +426,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : CH * R == 4 ? 384 : 512, TPR >
     px += step_bytes;
   }
   span_wait<0>();
-  if (a.partial == nullptr) return;
-  float* pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
-  float* pb = pw + static_cast<int64_t>(gridDim.x) * a.cols;
-  if constexpr (TPR > 0) {
-    // the block's groups: those of a warp by shuffles, the warps through shared memory
-    __shared__ float acc[8][32 * CH * 8];
-    const int warp = static_cast<int>(threadIdx.x) >> 5;
-#pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      if (pass) __syncthreads();
-#pragma unroll
-      for (int k = 0; k < CH; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float u[2];
-          f32x2_split(pass ? db[k][i] : dw[k][i], u[0], u[1]);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int o = 16; o >= TPR; o >>= 1) u[j] += __shfl_xor_sync(0xffffffffu, u[j], o);
-            if ((static_cast<int>(threadIdx.x) & 31) < TPR) acc[warp][(lane + k * TPR) * 8 + 2 * i + j] = u[j];
-          }
-        }
-      __syncthreads();
-      for (int32_t c = static_cast<int32_t>(threadIdx.x); c < a.cols; c += 256) {
-        float s = 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) s += acc[q][c];
-        (pass ? pb : pw)[c] = s;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int32_t c0 = (lane + k * step) * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float u[2], v[2];
-        f32x2_split(dw[k][i], u[0], u[1]);
-        f32x2_split(db[k][i], v[0], v[1]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (c0 + 2 * i + j < a.cols) {
-            pw[c0 + 2 * i + j] = u[j];
-            pb[c0 + 2 * i + j] = v[j];
-          }
-      }
-    }
-  }
+  store_column_sums<TPR, CH>(a, dw, db, lane, step);
 }
 
 // Column c of dw (y = 0) or db (y = 1): the parts in order, 32 threads each.

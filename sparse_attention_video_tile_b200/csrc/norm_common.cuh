@@ -22,12 +22,8 @@ using ptx::add_f32x2;
 using ptx::f32x2;
 using ptx::f32x2_split;
 using ptx::fma_f32x2;
+using ptx::mul_f32x2;
 
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t both(float v) { return f32x2(v, v); }
 __device__ __forceinline__ float sum_f32x2(uint64_t v) {
   float a, b;
