@@ -513,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   sum_dlambda(p.g, p.part, p.dlam, reinterpret_cast<float*>(smem));   // before any load into shared memory
+  fence_proxy_async();   // the loads (async proxy) write where the sums lay (generic proxy): after the barrier below
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kAbort);
   if (threadIdx.x == 0) {
     mbar_init(sb + S::kFixFull, 1);
