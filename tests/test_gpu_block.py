@@ -214,6 +214,37 @@ def test_captured_and_replayed():
         assert same(s2, eager) and same(g2, eg)
 
 
+def test_training_step_captured_and_replayed():
+    """Forward and gradients of the whole block through autograd in one graph: attention, head norm,
+    dropout, the residual norm, replayed on new inputs and a new generator state."""
+    static = [x.requires_grad_(i != 3) for i, x in enumerate(inputs(30))]
+    w = torch.randn(64, device="cuda").requires_grad_()
+    rng = torch.tensor([3, 1], device="cuda")
+
+    def step(q, k, v, do, lam):
+        a = A.sta_diff_attention(q, k, v, lam, GRID, TILE, WINDOWS, 0.18, norm_weight=w, dropout_p=0.25, rng=rng)
+        y, h = A.sta_layer_norm(a, residual=q, dropout_p=0.1, rng=rng)
+        return [y.detach(), h.detach()] + list(torch.autograd.grad(y, (q, k, v, lam, w), do))
+
+    side = torch.cuda.Stream()      # warm up off the default stream, as captures want it
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*static)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(*static)
+    for seed in (31, 32):
+        with torch.no_grad():
+            for dst, src in zip(static, inputs(seed)):
+                dst.copy_(src)
+            rng[1] = seed
+        g.replay()
+        torch.cuda.synchronize()
+        assert same(got, step(*static)), seed
+
+
 def test_two_streams_at_once():
     sets = [inputs(8 + i, d=128) for i in range(2)]
     want = []
