@@ -196,6 +196,37 @@ def test_dropout(rows, cols, dtype):
     close(y, want, tol + half(dt) * (want.abs() + tol) + tiny(dt), "dropout")
 
 
+@pytest.mark.parametrize("cols", [1536, 1153])
+def test_norm_past_two_to_the_31_elements(cols):
+    """The last rows of arrays of 2.2e9 elements equal the same rows alone, forward and backward, and
+    the mask there is dropout's own."""
+    rows = 2_200_000_000 // cols
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, r = (torch.empty(rows, cols, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    for t in (x, r):
+        for i in range(0, rows, 1 << 17):
+            part = t[i:i + (1 << 17)]
+            part.copy_(torch.randn(part.shape, device="cuda", generator=g))
+    assert x.numel() > 2 ** 31
+    w, rng = randn((cols,), torch.float32, 3, 0.3, 1.0), torch.tensor([5, 6], device="cuda")
+    y, h, mean, rstd = sta.sta_layer_norm_forward(x, w, residual=r)
+    dx = sta.sta_layer_norm_backward(r, h, mean, rstd, w, dh=x)[0]
+    tails = [slice(0, 512), slice(rows - rows % 8 - 512, rows)]   # start on a 16-byte boundary
+    for part in tails:
+        y1, h1, m1, s1 = sta.sta_layer_norm_forward(x[part].clone(), w, residual=r[part].clone())
+        assert torch.equal(y[part], y1) and torch.equal(h[part], h1)
+        assert torch.equal(mean[part], m1) and torch.equal(rstd[part], s1)
+        assert torch.equal(dx[part], sta.sta_layer_norm_backward(r[part].clone(), h1, m1, s1, w, dh=x[part].clone())[0])
+    del y, dx
+    masked = sta.sta_dropout_forward(x, 0.5, rng)
+    _, h, mean, rstd = sta.sta_layer_norm_forward(x, dropout_p=0.5, rng=rng)
+    assert torch.equal(h, masked)
+    dx, dres, _, _ = sta.sta_layer_norm_backward(r, h, mean, rstd, w, dropout_p=0.5, rng=rng)
+    dropped = sta.sta_dropout_forward(torch.ones_like(x), 0.5, rng) == 0
+    for part in tails:
+        assert torch.equal(dx[part] == 0, dropped[part] | (dres[part] == 0))
+
+
 # ------------------------------------------------------------------ padded attention, several items a CTA
 
 # batch, heads, d, grid, tile, windows of the heads in turn; items: batch x heads x 128-row blocks
