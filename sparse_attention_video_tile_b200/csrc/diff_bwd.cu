@@ -8,7 +8,9 @@
 // Three launches:
 //   * prep (HBM bound): q, k, v, dO copied into the tiled order of the padded latent,
 //     and per row -lse_m in log2 units and -D_m, with D_2 = dO . O_2 and
-//     D_1 = dO . out + lambda D_2 from the stored outputs.  Pad rows get P = 0
+//     D_1 = dO . out + lambda D_2 from the stored outputs.  These are bf16 (fp32 rows would be
+//     four times the forward's writes), so D_m is off by half steps of out and out2, and
+//     D_1's error grows with |lambda|, which D_1 itself does not.  Pad rows get P = 0
 //     (-lse = -inf) and D = 0, so that they add nothing anywhere;
 //   * dQ over query blocks and the key blocks of their windows;
 //   * dK, dV over key blocks and the query blocks that attend them; its first blocks also

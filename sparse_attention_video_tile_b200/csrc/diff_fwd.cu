@@ -26,16 +26,17 @@
 // reference.  p is at most 2^20, so O_m stays finite where |v| is below 2^107 divided by
 // the keys of the window.  With 60 that bound was 2^67; 8 raises it to 2^119, but
 // where scores spread by 11 in log2 it rescales so often that the kernel takes 8 to 14 %
-// longer (20: 4 %; ordinary scores: the same time with all three).  Scores, sums and O are fp32; P is
-// rounded to bf16 for the tensor cores (relative error 2^-8 at most per element, as in
-// the other attention kernels), l is summed from the unrounded p.
+// longer (20: 4 %; ordinary scores: the same time with all three).  Scores, sums and O are
+// fp32; P is rounded to bf16 for the tensor cores (relative error 2^-8 at most per element, as
+// in the other attention kernels; two bf16 parts would take 1024 more clocks of tensor work a
+// block and TMEM columns that d = 128 lacks), l is summed from the unrounded p.
 //
 // Bound: one warp's serial chain per block (scores into registers, maximum, 128
 // exponentials a thread, P out), 2626 clocks (active cycles counted by ncu over 1313.5 blocks
 // an SM, d = 128), against 2048 of MUFU (78 %) and 1536 of tensor work (24 M128 N128 K16 of 64
-// clocks, 58.5 %); the rest of the time is the clock under the power cap, 1.62 GHz.  Measured on 115 200 tokens, windows of 27
-// tiles of 384: d = 128, 24 heads 20.1 ms, 710 TFLOP/s counting 4 d a pair (12 heads 10.0);
-// d = 64, 12 heads 8.8 ms.  Sixteen softmax warps with half rows take 10.85 and 9.5 ms at 12
+// clocks, 58.5 %); the rest of the time is the clock under the power cap, 1.62 GHz.  Measured
+// on 115 200 tokens, windows of 27 tiles of 384: d = 128, 24 heads 20.1 to 20.8 ms, 690 to 710
+// TFLOP/s counting 4 d a pair (12 heads 10.0, 8.9 in short runs below the cap); d = 64, 12 heads 8.8 ms.  Sixteen softmax warps with half rows take 10.85 and 9.5 ms at 12
 // heads, P stored in parts as it is made 11.6 and 9.8, 2 or 4 of 8 pairs of exponentials on
 // the FMA pipe 10.6 and 12.1 (d = 128).
 #include "diff_common.cuh"

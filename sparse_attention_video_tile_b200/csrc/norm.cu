@@ -9,8 +9,8 @@
 // of squared differences from the mean, with no cancellation and no second read; all
 // sums are fp32.  y is taken from the fp32 h, before h is rounded for its store.
 //
-// Measured (a plain copy moves 6400 GB/s): 1 382 400 x 128 bf16 in 116 us, 6100 GB/s; 57 600 x
-// 1536 bf16 with residual and dropout in 115 us, 6150 GB/s; fp32 5000 to 5900 GB/s, from 2048
+// Measured (a plain copy moves 6400 GB/s): 1 382 400 x 128 bf16 in 118 us, 6000 GB/s; 57 600 x
+// 1536 bf16 with residual and dropout in 119 us, 5950 GB/s; fp32 5000 to 5900 GB/s, from 2048
 // columns on 4100 to 5900.  Rows of an odd width pass shared memory four times and are bound by
 // that, their shifts and their barriers: 36 377 x 1153 bf16 2000 GB/s, fp32 3290; 173 318 x 121 fp32
 // 4360; 2 M x 20 bf16 2160.

@@ -12,7 +12,7 @@
 //
 // Measured (a plain copy moves 6400 GB/s): 1 382 400 x 128 bf16 in 174 us, 6100 GB/s; 57 600 x
 // 1536 bf16 with the gradient that reaches h, dropout and both outputs in 180 us, 4900 GB/s, bound
-// by the generator's and the row's instructions at 16 warps an SM; fp32 4500 to 5900 GB/s; odd
+// by the generator's and the row's instructions at 12 warps an SM; fp32 4500 to 5900 GB/s; odd
 // widths from 9 columns on 1000 to 4000 GB/s (36 377 x 1153 bf16 2190, fp32 3390), bound by their
 // passes through shared memory and the barriers.
 #include "norm_common.cuh"
