@@ -203,8 +203,9 @@ def sta_diff_attention(q, k, v, lam, grid, tile, window_per_head: Sequence, scal
     Q1, K1 the first d/2 columns of q and k, Q2, K2 the last d/2, ``lam`` fp32 [heads]
     (any function of learned vectors; it receives a gradient) and scale 1 / sqrt(d / 2)
     by default.  Grids that are not tile multiples are padded with masking.  The method keeps
-    lam around 0.2 to 0.8; with |lam| far above 1 the first map's dq and dk lose accuracy in
-    proportion to it, since their row sums come from the stored bf16 outputs.
+    lam around 0.2 to 0.8; with |lam| above 10 the first map's dq and dk lose accuracy in
+    proportion to it (17 times the usual error at 100), since their row sums come from the
+    stored bf16 outputs.
 
     With ``norm_weight`` (and ``norm_bias``), both [d], every head's output row then
     goes through ``sta_layer_norm`` (a factor such as 1 - lambda_init belongs in the weight).

@@ -182,7 +182,7 @@ def sta_layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, residua
 def sta_layer_norm_bwd_workspace(rows: int, cols: int) -> int:
     """Bytes of workspace that ``sta_layer_norm_bwd`` needs when it makes a weight's or bias's gradient."""
     rows, cols = int(rows), int(cols)
-    n = load_library().sta_layer_norm_bwd_workspace(rows, cols) if rows < 2 ** 63 and abs(cols) <= _INT32_MAX else -1
+    n = load_library().sta_layer_norm_bwd_workspace(rows, cols) if max(abs(rows) >> 32, abs(cols)) <= _INT32_MAX else -1
     if n < 0:
         raise StaError(4, "sta_layer_norm_bwd_workspace")
     return int(n)

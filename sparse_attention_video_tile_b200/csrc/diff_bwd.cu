@@ -164,7 +164,8 @@ __device__ __forceinline__ void sum_dlambda(const DiffGeo& g, const float* part,
 // in columns of their own (256-383), dQ_1 and dQ_2 (384-511).  Scores are free again
 // once they are in registers and dP once both maps have read it, so the next block's
 // S and dP run under this block's exponentials.  Bound by that chain of the elementwise
-// warps, 3547 clocks a block (ncu, active cycles; 1.69 GHz).  Measured, 6 heads of 115 200 tokens, windows of 27 tiles of 384:
+// warps, 3547 clocks a block (ncu, active cycles; 1.69 GHz).  Measured, 6 heads of 115 200
+// tokens, windows of 27 tiles of 384:
 // 5.84 ms at d = 128, 5.28 at d = 64 (5.42 with two stages of K and V instead of four).
 
 template <int D>

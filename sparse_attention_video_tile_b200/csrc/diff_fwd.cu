@@ -36,9 +36,10 @@
 // an SM, d = 128), against 2048 of MUFU (78 %) and 1536 of tensor work (24 M128 N128 K16 of 64
 // clocks, 58.5 %); the rest of the time is the clock under the power cap, 1.62 GHz.  Measured
 // on 115 200 tokens, windows of 27 tiles of 384: d = 128, 24 heads 20.1 to 20.8 ms, 690 to 710
-// TFLOP/s counting 4 d a pair (12 heads 10.0, 8.9 in short runs below the cap); d = 64, 12 heads 8.8 ms.  Sixteen softmax warps with half rows take 10.85 and 9.5 ms at 12
-// heads, P stored in parts as it is made 11.6 and 9.8, 2 or 4 of 8 pairs of exponentials on
-// the FMA pipe 10.6 and 12.1 (d = 128).
+// TFLOP/s counting 4 d a pair (12 heads 10.0, 8.9 in short runs below the cap); d = 64, 12
+// heads 8.8 ms.  Sixteen softmax warps with half rows take 10.85 and 9.5 ms at 12 heads, P
+// stored in parts as it is made 11.6 and 9.8, 2 or 4 of 8 pairs of exponentials on the FMA
+// pipe 10.6 and 12.1 (d = 128).
 #include "diff_common.cuh"
 
 namespace sta {
