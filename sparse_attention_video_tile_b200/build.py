@@ -23,7 +23,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cu", "api_diff.cu", "api_norm.cu", "attention.cu", "backward.cu", "diff_bwd.cu", "diff_fwd.cu", "noalloc.cu",
            "norm.cu", "norm_bwd.cu", "reorder.cu", "schedule.cpp"]
-HEADERS = ["checks.h", "diff.h", "diff_common.cuh", "internal.h", "norm.h", "norm_common.cuh", "philox.cuh", "ptx.cuh"]
+HEADERS = ["checks.h", "diff.h", "diff_common.cuh", "internal.h", "norm.h", "norm_common.cuh", "packed.cuh", "philox.cuh", "ptx.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

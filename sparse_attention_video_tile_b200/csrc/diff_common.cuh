@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "diff.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 namespace sta {

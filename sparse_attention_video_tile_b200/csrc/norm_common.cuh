@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "norm.h"
+#include "packed.cuh"
 #include "philox.cuh"
 #include "ptx.cuh"
 

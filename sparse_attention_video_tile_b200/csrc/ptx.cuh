@@ -361,13 +361,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// a * b on both halves (round to nearest even)
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // 2^x for a packed pair on the FMA pipe: the same reduction and cubic as
 // exp2_poly3, with packed fp32x2 arithmetic (one instruction per pair).  For
 // finite x in [-125, 127]; callers keep x inside that range.
